@@ -19,6 +19,10 @@
  *   flux_kv_write              append / fill a full cache or an SA layer's ring
  *   flux_attn_decode_sa_compact  SA decode over the ring (sink + last W blocks)
  *   flux_attn_decode_append    append the step's token + decode, one launch
+ *   flux_build_page_table      block tables, slot map, positions of a paged cache
+ *   flux_qk_norm_rope          per-head RMS norm of q and k + position rotation
+ *   flux_kv_write_q4 / _read_q4  rows into / out of a paged 4-bit KV cache
+ *   flux_attn_decode_q4        decode over that cache, FA or SA per layer_mode
  *
  * Conventions shared by every entry point
  *   - Every tensor pointer is a DEVICE pointer owned by the caller; the
@@ -375,6 +379,116 @@ int flux_attn_decode_noalloc(const uint16_t* q, const uint16_t* k_cache, const u
  * and SA window (host-only query; no device work). */
 int flux_decode_workspace_bytes(flux_ctx* ctx, int B, int Hq, int Hkv, int d, int S_max,
                                 int sink_blocks, int window_blocks, int block, size_t* bytes);
+
+/* --------------------------------------------------------------------------
+ * Paged 4-bit KV cache.  The pages have no counterpart of these calls; they
+ * stand between the projection's q, k, v and the decode attention of a server
+ * whose requests differ in length: build_page_table -> qk_norm_rope ->
+ * kv_write_q4 -> attn_decode_q4, one stream, no host synchronisation; every
+ * call can be captured in a CUDA graph and reads its lengths at replay.
+ * Each of them needs the ctx's device to be the current one (INVALID_ARG).
+ *
+ * Cache: kv_pool uint8 [num_pages, Hkv, page_size / 16, 18 * d], 16-byte
+ * aligned; page_size a multiple of 16 up to 65536, d 64 or 128.  A page holds
+ * page_size tokens of every kv head, K and V, as records of 16 tokens with
+ * their codes and scales (4.5 bits per value: 2304 bytes per 16 tokens and kv
+ * head at d 128, against 8192 in bf16).  The bytes inside a record are the
+ * library's own order.  What a record stands for: in each group of 32
+ * consecutive channels of a row, with a = max|x|,
+ *   scale = a / 7 cut towards zero to 5 significant bits (bf16),
+ *   code  = x / scale rounded to the nearest whole number, ties to even (-7..7),
+ * and the stored value is code * scale, exactly a bf16 number; writing values
+ * that were read back stores the same bits.  A group with a < 2^-100 is stored
+ * as zeros; one with a > 2^120, an infinity or a NaN as NaN throughout.
+ * Slot = page * page_size + offset in the page: a token's place, 64-bit.
+ *
+ * flux_build_page_table: block tables, slot map and positions of the step in
+ * which request b grows from old_lens[b] to new_lens[b] tokens (0 = not there
+ * yet), from a free list.  np(x) = ceil(x / page_size).
+ *   old_lens, new_lens [B] int32; free_pages [n_free] int32; cursor [1] int32:
+ *   entries of free_pages already handed out; cursor_out [1]: the same after
+ *   the call (may be cursor itself).
+ *   page_table [B, max_pages] int32, in and out: entries np(old) .. np(new) - 1
+ *   of each request are written, taken from the free list in request order;
+ *   the others are left as they were.
+ *   window_pages > 0: a ring for SA layers (cf. flux_kv_write).  A request
+ *   holds at most sink_pages + window_pages pages; logical page j >= that many
+ *   shares the physical page of j - window_pages, so the table still has one
+ *   entry per logical page and an SA decode whose sink and window blocks fit
+ *   the ring's pages (block a multiple of page_size) finds its tokens.
+ *   window_pages = 0: no ring (sink_pages must be 0).
+ *   slots [n_slots] int64, positions [n_slots] int32 out: the new tokens,
+ *   request after request; token i is token positions[i] of its request and
+ *   goes to slots[i]; -1 for a token that the ring no longer holds at the new
+ *   length, and -1 with position 0 behind the last token.
+ *   cu_new [B + 1] int32 out (optional): tokens before each request.
+ * Device-checked: old < 0, new < old, np(new) > max_pages; more new tokens
+ * than n_slots or more pages than the list has left (then, or with a cursor
+ * outside the list, nothing is handed out: the table and the cursor stay, all
+ * slots are -1, cu_new is 0); a negative page id where one is needed (slot -1).
+ * B <= 8192.
+ *
+ * flux_qk_norm_rope: q and k of N tokens from the projection's output to what
+ * the attention calls take.  Per head: y = x / sqrt(mean(x^2) + eps) * weight
+ * (weights [d] bf16 for q and for k; both NULL: no norm), then the rotation of
+ * channel pairs by position * inv_freq[i]: (a, b) -> (a cos - b sin, b cos + a
+ * sin), pair i = channels (i, i + rot / 2), or (2i, 2i + 1) with interleaved
+ * = 1; channels >= rot pass.  rot a multiple of 16, 16 <= rot <= d.
+ *   q [N, Hq, d], k [N, Hkv, d] bf16, a token's heads contiguous, q_stride /
+ *   k_stride elements from token to token (views of a packed projection);
+ *   q_out, k_out likewise; an output may be its input (same pointer and
+ *   stride), any other overlap is undefined.  Pointers 16-byte aligned,
+ *   strides multiples of 8 and at least the row.
+ *   positions [N] int32, inv_freq [rot / 2] fp32.  fp32 arithmetic, angles in
+ *   fp64; one rounding to bf16.
+ *
+ * flux_kv_write_q4: k_src, v_src [N, Hkv, d] bf16 (strides as above) to
+ * slots[n] of the cache; a negative slot skips the token, a slot beyond the
+ * cache is a device-checked error and skips it.  A slot may appear once per
+ * call.  flux_kv_read_q4: the stored values of slots[n] to k_dst, v_dst [N,
+ * Hkv, d] bf16, contiguous; rows of skipped slots are left as they were.
+ *
+ * flux_attn_decode_q4: flux_attn_decode over the cache.  Token u of sequence b
+ * is at page_table[b][u / page_size], offset u % page_size; seqlens[b] counts
+ * the tokens (0: zero output, lse -inf) and may not pass max_pages * page_size
+ * (device-checked as there).  A page id outside [0, num_pages) where live
+ * tokens are read is a device-checked error and leaves those tokens out; other
+ * entries are never read.  Bytes behind a sequence's last token are never
+ * used, whatever they hold.  q, o, lse, layer_mode, sink / window / block,
+ * scale and the group limits as flux_attn_decode.  Split partials live in the
+ * ctx workspace (flux_decode_q4_workspace_bytes). */
+int flux_build_page_table(flux_ctx* ctx, const int32_t* old_lens, const int32_t* new_lens, int B,
+                          int page_size, int sink_pages, int window_pages,
+                          const int32_t* free_pages, int n_free, const int32_t* cursor,
+                          int32_t* cursor_out, int32_t* page_table, int max_pages,
+                          int64_t* slots, int32_t* positions, int n_slots, int32_t* cu_new,
+                          flux_stream_t stream);
+
+int flux_qk_norm_rope(flux_ctx* ctx, const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                      int64_t k_stride, uint16_t* q_out, int64_t q_out_stride, uint16_t* k_out,
+                      int64_t k_out_stride, int N, int Hq, int Hkv, int d,
+                      const uint16_t* q_weight, const uint16_t* k_weight, float eps,
+                      const int32_t* positions, const float* inv_freq, int rot, int interleaved,
+                      flux_stream_t stream);
+
+int flux_kv_write_q4(flux_ctx* ctx, const uint16_t* k_src, int64_t k_stride,
+                     const uint16_t* v_src, int64_t v_stride, const int64_t* slots, int N,
+                     int Hkv, int d, uint8_t* kv_pool, int num_pages, int page_size,
+                     flux_stream_t stream);
+
+int flux_kv_read_q4(flux_ctx* ctx, const uint8_t* kv_pool, int num_pages, int page_size,
+                    const int64_t* slots, int N, int Hkv, int d, uint16_t* k_dst,
+                    uint16_t* v_dst, flux_stream_t stream);
+
+int flux_attn_decode_q4(flux_ctx* ctx, const uint16_t* q, const uint8_t* kv_pool, int num_pages,
+                        int page_size, const int32_t* page_table, int max_pages,
+                        const int32_t* seqlens, uint16_t* o, float* lse, int B, int Hq, int Hkv,
+                        int d, const uint8_t* layer_mode, int layer, int sink_blocks,
+                        int window_blocks, int block, float scale, flux_stream_t stream);
+
+/* Workspace bytes flux_attn_decode_q4 needs on this ctx's device at head_dim d,
+ * for any batch and length (host-only query). */
+int flux_decode_q4_workspace_bytes(flux_ctx* ctx, int d, size_t* bytes);
 
 #ifdef __cplusplus
 }

@@ -13,6 +13,7 @@
 
 #include "flux.h"
 #include "kernels.h"
+#include "q4.h"
 
 struct flux_ctx {
   int device;
@@ -373,7 +374,10 @@ int flux_ctx_check(flux_ctx* c, flux_stream_t stream) {
       return fail(FLUX_ERR_DEVICE_CHECK,
                   "block-index list entry out of range or a row not strictly ascending");
     case flux::DEV_ERR_CAPACITY:
-      return fail(FLUX_ERR_DEVICE_CHECK, "block-index nnz exceeds the col capacity");
+      return fail(FLUX_ERR_DEVICE_CHECK, "block-index nnz exceeds the col capacity, or a page table step "
+                                         "needs more slots or pages than there are");
+    case flux::DEV_ERR_PAGE:
+      return fail(FLUX_ERR_DEVICE_CHECK, "page or slot outside the paged cache");
     default:
       return fail(FLUX_ERR_DEVICE_CHECK, "device error word %d", word);
   }
@@ -725,4 +729,192 @@ extern "C" int flux_selftest_bounded_wait(flux_ctx* c, int spin_limit_ms, int* w
   flux::DevStatus st{c->err, static_cast<long long>(spin_limit_ms) * 1000000LL};
   const cudaError_t e = flux::launch_selftest_wait(st, waited_us, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FLUX_OK : cuda_fail(e, "flux_selftest_bounded_wait: launch");
+}
+
+// ---------------------------------------------------------------------------
+// Paged 4-bit KV cache.
+namespace {
+
+// The caller's current device must be the ctx's: a launch goes to the current one.
+int check_device(const flux_ctx* c, const char* name) {
+  int dev = -1;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, name);
+  if (dev != c->device)
+    return fail(FLUX_ERR_INVALID_ARG, "%s: the current device is %d, the ctx is on %d", name, dev,
+                c->device);
+  return FLUX_OK;
+}
+
+// The checks that every call on a 4-bit cache shares.
+int check_pool(const char* name, const uint8_t* pool, int num_pages, int page_size, int Hkv, int d) {
+  if (d != 64 && d != 128)
+    return fail(FLUX_ERR_UNSUPPORTED, "%s: head_dim %d (supported: 64, 128)", name, d);
+  if (Hkv < 1 || num_pages < 1) return fail(FLUX_ERR_SHAPE, "%s: sizes must be positive", name);
+  if (page_size < 16 || page_size % 16 != 0 || page_size > 65536)
+    return fail(FLUX_ERR_UNSUPPORTED, "%s: page_size %d (a multiple of 16 up to 65536)", name,
+                page_size);
+  if (!aligned16(pool)) return fail(FLUX_ERR_INVALID_ARG, "%s: kv_pool must be 16-byte aligned", name);
+  return FLUX_OK;
+}
+
+// A [N, H, d] row view: heads contiguous, 16-byte vectors.
+bool row_view_ok(const void* p, int64_t stride, int H, int d) {
+  return aligned16(p) && stride % 8 == 0 && stride >= static_cast<int64_t>(H) * d;
+}
+
+}  // namespace
+
+extern "C" int flux_build_page_table(flux_ctx* c, const int32_t* old_lens, const int32_t* new_lens,
+                                     int B, int page_size, int sink_pages, int window_pages,
+                                     const int32_t* free_pages, int n_free, const int32_t* cursor,
+                                     int32_t* cursor_out, int32_t* page_table, int max_pages,
+                                     int64_t* slots, int32_t* positions, int n_slots,
+                                     int32_t* cu_new, flux_stream_t stream) {
+  const char* name = "flux_build_page_table";
+  if (!c || !old_lens || !new_lens || !free_pages || !cursor || !cursor_out || !page_table ||
+      !slots || !positions)
+    return fail(FLUX_ERR_INVALID_ARG, "%s: null pointer argument", name);
+  if (B < 1 || n_free < 1 || max_pages < 1 || n_slots < 1)
+    return fail(FLUX_ERR_SHAPE, "%s: sizes must be positive", name);
+  if (B > flux::kPageTableMaxB)
+    return fail(FLUX_ERR_UNSUPPORTED, "%s: B %d above %d", name, B, flux::kPageTableMaxB);
+  if (page_size < 16 || page_size % 16 != 0 || page_size > 65536)
+    return fail(FLUX_ERR_UNSUPPORTED, "%s: page_size %d (a multiple of 16 up to 65536)", name,
+                page_size);
+  if (sink_pages < 0 || window_pages < 0 || (window_pages == 0 && sink_pages != 0) ||
+      sink_pages > (1 << 28) || window_pages > (1 << 28))
+    return fail(FLUX_ERR_INVALID_ARG, "%s: bad sink / window pages", name);
+  int rc = check_device(c, name);
+  if (rc != FLUX_OK) return rc;
+  const flux::PageTableLaunch p{old_lens, new_lens, B, page_size, sink_pages, window_pages,
+                                free_pages, n_free, cursor, cursor_out, page_table, max_pages,
+                                slots, positions, n_slots, cu_new, c->tickets, c->err};
+  const cudaError_t e = flux::launch_page_table(p, c->num_sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FLUX_OK : cuda_fail(e, name);
+}
+
+extern "C" int flux_qk_norm_rope(flux_ctx* c, const uint16_t* q, int64_t q_stride,
+                                 const uint16_t* k, int64_t k_stride, uint16_t* q_out,
+                                 int64_t q_out_stride, uint16_t* k_out, int64_t k_out_stride,
+                                 int N, int Hq, int Hkv, int d, const uint16_t* q_weight,
+                                 const uint16_t* k_weight, float eps, const int32_t* positions,
+                                 const float* inv_freq, int rot, int interleaved,
+                                 flux_stream_t stream) {
+  const char* name = "flux_qk_norm_rope";
+  if (!c || !q || !k || !q_out || !k_out || !positions || !inv_freq)
+    return fail(FLUX_ERR_INVALID_ARG, "%s: null pointer argument", name);
+  if ((q_weight == nullptr) != (k_weight == nullptr))
+    return fail(FLUX_ERR_INVALID_ARG, "%s: give both norm weights or neither", name);
+  if (N < 1 || Hq < 1 || Hkv < 1) return fail(FLUX_ERR_SHAPE, "%s: sizes must be positive", name);
+  if (d != 64 && d != 128)
+    return fail(FLUX_ERR_UNSUPPORTED, "%s: head_dim %d (supported: 64, 128)", name, d);
+  if (rot < 16 || rot > d || rot % 16 != 0)
+    return fail(FLUX_ERR_UNSUPPORTED, "%s: rot %d (a multiple of 16 up to %d)", name, rot, d);
+  if (interleaved != 0 && interleaved != 1)
+    return fail(FLUX_ERR_INVALID_ARG, "%s: interleaved must be 0 or 1", name);
+  if (!(eps >= 0.f) || eps > 3.0e38f)
+    return fail(FLUX_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", name);
+  if (static_cast<long long>(N) * (static_cast<long long>(Hq) + Hkv) > (1LL << 31))
+    return fail(FLUX_ERR_SHAPE, "%s: N * (Hq + Hkv) above 2^31", name);
+  if (!row_view_ok(q, q_stride, Hq, d) || !row_view_ok(k, k_stride, Hkv, d) ||
+      !row_view_ok(q_out, q_out_stride, Hq, d) || !row_view_ok(k_out, k_out_stride, Hkv, d) ||
+      (q_weight && (!aligned16(q_weight) || !aligned16(k_weight))))
+    return fail(FLUX_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned, strides multiples of "
+                "8 and at least H * d", name);
+  int rc = check_device(c, name);
+  if (rc != FLUX_OK) return rc;
+  const flux::NormRopeLaunch p{q, k, q_stride, k_stride, q_out, k_out, q_out_stride, k_out_stride,
+                               q_weight, k_weight, eps, positions, inv_freq, rot, interleaved,
+                               N, Hq, Hkv, d};
+  const cudaError_t e = flux::launch_norm_rope(p, c->num_sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FLUX_OK : cuda_fail(e, name);
+}
+
+extern "C" int flux_kv_write_q4(flux_ctx* c, const uint16_t* k_src, int64_t k_stride,
+                                const uint16_t* v_src, int64_t v_stride, const int64_t* slots,
+                                int N, int Hkv, int d, uint8_t* kv_pool, int num_pages,
+                                int page_size, flux_stream_t stream) {
+  const char* name = "flux_kv_write_q4";
+  if (!c || !k_src || !v_src || !slots || !kv_pool)
+    return fail(FLUX_ERR_INVALID_ARG, "%s: null pointer argument", name);
+  if (N < 1) return fail(FLUX_ERR_SHAPE, "%s: sizes must be positive", name);
+  int rc = check_pool(name, kv_pool, num_pages, page_size, Hkv, d);
+  if (rc != FLUX_OK) return rc;
+  if (static_cast<long long>(N) * Hkv > (1LL << 31))
+    return fail(FLUX_ERR_SHAPE, "%s: N * Hkv above 2^31", name);
+  if (!row_view_ok(k_src, k_stride, Hkv, d) || !row_view_ok(v_src, v_stride, Hkv, d))
+    return fail(FLUX_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned, strides multiples of "
+                "8 and at least Hkv * d", name);
+  if ((rc = check_device(c, name)) != FLUX_OK) return rc;
+  const flux::KvQ4Launch p{k_src, v_src, k_stride, v_stride, nullptr, nullptr, slots, N, Hkv, d,
+                           kv_pool, num_pages, page_size, c->err};
+  const cudaError_t e = flux::launch_kv_write_q4(p, c->num_sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FLUX_OK : cuda_fail(e, name);
+}
+
+extern "C" int flux_kv_read_q4(flux_ctx* c, const uint8_t* kv_pool, int num_pages, int page_size,
+                               const int64_t* slots, int N, int Hkv, int d, uint16_t* k_dst,
+                               uint16_t* v_dst, flux_stream_t stream) {
+  const char* name = "flux_kv_read_q4";
+  if (!c || !k_dst || !v_dst || !slots || !kv_pool)
+    return fail(FLUX_ERR_INVALID_ARG, "%s: null pointer argument", name);
+  if (N < 1) return fail(FLUX_ERR_SHAPE, "%s: sizes must be positive", name);
+  int rc = check_pool(name, kv_pool, num_pages, page_size, Hkv, d);
+  if (rc != FLUX_OK) return rc;
+  if (static_cast<long long>(N) * Hkv > (1LL << 31))
+    return fail(FLUX_ERR_SHAPE, "%s: N * Hkv above 2^31", name);
+  if (!aligned16(k_dst) || !aligned16(v_dst))
+    return fail(FLUX_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", name);
+  if ((rc = check_device(c, name)) != FLUX_OK) return rc;
+  const flux::KvQ4Launch p{nullptr, nullptr, 0, 0, k_dst, v_dst, slots, N, Hkv, d,
+                           const_cast<uint8_t*>(kv_pool), num_pages, page_size, c->err};
+  const cudaError_t e = flux::launch_kv_read_q4(p, c->num_sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FLUX_OK : cuda_fail(e, name);
+}
+
+extern "C" int flux_decode_q4_workspace_bytes(flux_ctx* c, int d, size_t* bytes) {
+  if (!c || !bytes || (d != 64 && d != 128))
+    return fail(FLUX_ERR_INVALID_ARG, "flux_decode_q4_workspace_bytes: bad arguments");
+  *bytes = flux::decode_q4_workspace_bytes(d, c->num_sms);
+  return FLUX_OK;
+}
+
+extern "C" int flux_attn_decode_q4(flux_ctx* c, const uint16_t* q, const uint8_t* kv_pool,
+                                   int num_pages, int page_size, const int32_t* page_table,
+                                   int max_pages, const int32_t* seqlens, uint16_t* o, float* lse,
+                                   int B, int Hq, int Hkv, int d, const uint8_t* layer_mode,
+                                   int layer, int sink_blocks, int window_blocks, int block,
+                                   float scale, flux_stream_t stream) {
+  const char* name = "flux_attn_decode_q4";
+  if (!c) return fail(FLUX_ERR_INVALID_ARG, "%s: null context", name);
+  if (!q || !kv_pool || !page_table || !seqlens || !o)
+    return fail(FLUX_ERR_INVALID_ARG, "%s: null tensor", name);
+  if (B < 1 || Hq < 1 || max_pages < 1)
+    return fail(FLUX_ERR_SHAPE, "%s: sizes must be positive", name);
+  int rc = check_pool(name, kv_pool, num_pages, page_size, Hkv, d);
+  if (rc != FLUX_OK) return rc;
+  if (Hq % Hkv != 0 || Hq / Hkv > flux::kDecodeMaxGroup)
+    return fail(FLUX_ERR_UNSUPPORTED, "%s: Hq/Hkv must be a whole number from 1 to %d (%d, %d)",
+                name, flux::kDecodeMaxGroup, Hq, Hkv);
+  if (block < 1 || sink_blocks < 0 || window_blocks < 1)
+    return fail(FLUX_ERR_INVALID_ARG, "%s: bad block / sink / window", name);
+  if (layer_mode && layer < 0) return fail(FLUX_ERR_INVALID_ARG, "%s: negative layer", name);
+  if (!(scale == scale) || scale <= 0.f || scale > 3.0e38f)
+    return fail(FLUX_ERR_INVALID_ARG, "%s: scale must be finite and positive", name);
+  if (static_cast<long long>(B) * Hkv > kMaxTickets)
+    return fail(FLUX_ERR_SHAPE, "%s: B * Hkv = %lld exceeds %d", name,
+                static_cast<long long>(B) * Hkv, kMaxTickets);
+  if (!aligned16(q) || !aligned16(o))
+    return fail(FLUX_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", name);
+  if ((rc = check_device(c, name)) != FLUX_OK) return rc;
+  const size_t need = flux::decode_q4_workspace_bytes(d, c->num_sms);
+  if (need > c->workspace_bytes)
+    return fail(FLUX_ERR_SHAPE, "%s: workspace %zu < %zu bytes", name, c->workspace_bytes, need);
+  const flux::DecodeQ4Launch p{q, kv_pool, num_pages, page_size, page_table, max_pages, seqlens,
+                               o, lse, B, Hq, Hkv, d, layer_mode, layer, sink_blocks,
+                               window_blocks, block, scale, static_cast<float*>(c->workspace),
+                               c->tickets, status_of(c)};
+  const cudaError_t e = flux::launch_decode_q4(p, c->num_sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FLUX_OK : cuda_fail(e, name);
 }
