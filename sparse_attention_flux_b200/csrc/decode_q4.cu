@@ -2,133 +2,659 @@
 // q4.h): one query token per sequence, the routing bit, the SA mask and the
 // output of decode.cu.
 //
-// One CTA per (kv head, sequence); its warps take 16-token records in turn.  A
-// warp's lane owns D / 32 channels, scores are warp sums, and each query head of
-// the group keeps the running maximum and sum of its softmax.  The warps'
-// partials are merged in shared memory at the end.
+// Bound: the cache bytes (18 d per 16 tokens and kv head); the work per byte
+// is the unpacking, so the kernel is built to keep HBM busy with as few issued
+// instructions per record as possible.
+//
+// Work split.  The live records of all (sequence, kv head) rows are laid end to
+// end and cut into equal ranges, one per CTA (two CTAs per SM, one wave), so a
+// ragged batch loads every SM alike.  A CTA walks its range row by row; within
+// a row its consumer warps take records in turn and merge at the row's
+// end in shared memory.  A row that crosses a range border (at most the first
+// and the last of a CTA) leaves a partial in the workspace; the CTA that
+// delivers a row's last partial (a ticket) merges them in range order, so the
+// result does not depend on timing.
+//
+// Stream.  A producer warp walks the same range ahead of the consumers, one
+// lane per ring stage: it looks up the record's page and copies the record (one
+// contiguous bulk copy) into shared memory, 28 records in flight per CTA.
+//
+// Arithmetic per record, one warp, warp MMAs (m16n8k16, bf16, fp32 sums):
+//   S = K q^T: the 16 tokens are the rows, the group's query heads (up to 8)
+//     the columns.  A code's 4 bits are a bf16 mantissa's upper bits, so one
+//     AND-OR per pair makes operands 16 + u, u = code + 8; the products of one
+//     32-channel group start from -24 sum(q) and are multiplied by the token's
+//     scale in fp32.
+//   O^T += V^T P^T: the lane's channels are the rows; (16 + u) s - 24 s is one
+//     packed fma and exactly the stored value.  P is rounded to bf16 for the
+//     MMA (the softmax sum keeps fp32 values) and turned by movmatrix.
+// The softmax runs against a reference that only grows when a score passes it
+// by 8 (in log2 units): p <= 2^8, and the common record needs no rescaling and
+// one vote.
 #include "q4.h"
 
 namespace flux {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kMaxG = 8;
+constexpr int kWarps = 7;                   // consumer warps: with the producer 16 warps per SM, 128
+                                            // registers each (8 + 1 would leave 96, and spills)
+constexpr int kThreads = 32 * kWarps + 32;  // + the producer warp
+constexpr int kDepth = 4;                   // ring stages per warp
+constexpr int kStages = kDepth * kWarps;    // records in flight per CTA, a producer lane each.  A stage
+                                            // belongs to one warp: a wait tells only the parity of a
+                                            // phase, so no other may come to it a round early
+static_assert(kStages <= 32 && (kDepth & (kDepth - 1)) == 0, "one producer lane per stage");
+constexpr int kCtasPerSm = 2;
+constexpr float kGrow = 8.f;                // log2 growth of a score that is tolerated
+constexpr float kLowest = -3.0e38f;         // reference of a row without tokens: finite, so that
+                                            // no difference of two references is NaN
+
+// Raw accumulator order: float4 (tile m, lane 4 g + t) = channels g D/8 + 2 m
+// and + 1 of heads 2 t and 2 t + 1, as the MMA leaves them.
+template <int D>
+struct Q4Smem {
+  static constexpr int NT = D / 16;                       // channel tiles
+  static constexpr int RING = kStages * Q4Layout<D>::BYTES;
+  static constexpr int PART4 = NT * 32;                   // float4 per partial
+  static constexpr int ACC = kWarps * PART4 * 16;
+  static constexpr int ML = RING + ACC;                   // m, l [warp][8]
+  static constexpr int FIN = ML + 2 * kWarps * 8 * 4;     // weights and 1 / l of the final merge
+  static constexpr int BAR = FIN + 2 * 8 * 4;
+  static constexpr int FLAG = BAR + 2 * kStages * 8;
+  static constexpr int MISC = FLAG + kStages * 4;         // start row, totals, ticket
+  static constexpr int BYTES = MISC + 64;
+};
+
+// The live records of one sequence: [0, head) and [tail, end) of its records,
+// `count` of them; the tokens inside them are live below n_sink and from win on.
+struct Live {
+  int s, n_sink, win, head, tail, count;
+};
+
+__device__ __forceinline__ Live live_of(const DecodeQ4Launch& a, int b, bool fa) {
+  Live v;
+  int s = a.seqlens[b];
+  if (s < 0 || s > static_cast<long long>(a.max_pages) * a.page_size) s = 0;
+  const int recs = s > 0 ? (s - 1) / kQ4Rec + 1 : 0;
+  v.s = s;
+  v.n_sink = s;
+  v.win = 0;
+  v.head = recs;
+  v.tail = recs;
+  if (!fa && s > 0) {
+    const int nb = (s - 1) / a.block + 1;
+    v.n_sink = static_cast<int>(min(static_cast<long long>(a.sink_blocks) * a.block,
+                                    static_cast<long long>(s)));
+    v.win = max(0, nb - a.window_blocks) * a.block;
+    v.head = v.n_sink > 0 ? (v.n_sink - 1) / kQ4Rec + 1 : 0;
+    v.tail = max(v.win / kQ4Rec, v.head);
+  }
+  v.count = v.head + recs - v.tail;
+  return v;
+}
+
+// Walks rows (b, g) in order, skipping sequences without records.
+struct Walk {
+  int b, g;
+  long long row0;          // the row's first record in the flat order
+  Live v;
+};
+
+__device__ __forceinline__ void next_row(const DecodeQ4Launch& a, bool fa, Walk& w) {
+  w.row0 += w.v.count;
+  if (++w.g == a.Hkv) {
+    w.g = 0;
+    do {
+      ++w.b;
+      if (w.b >= a.B) {    // behind the last row: never reached while records remain
+        w.v.count = 0x7fffffff;
+        return;
+      }
+      w.v = live_of(a, w.b, fa);
+    } while (w.v.count == 0);
+  }
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t x, uint32_t y, uint32_t z) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(y), "r"(z));
+  return r;
+}
+
+// d = a b + c with c held elsewhere.
+__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1, float c0, float c1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%11,%10,%11};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
+
+constexpr uint32_t kCode = 0x00780078u;     // the upper four mantissa bits of both halves
+constexpr uint32_t kBase = 0x41804180u;     // 16.0, 16.0
+
+// Operand pairs of a K word (stored rotated left by 3): channels 2 i, 2 i + 1.
+template <int I>
+__device__ __forceinline__ uint32_t k_pair(uint32_t w) {
+  const uint32_t x = I == 0 ? w : (I == 3 ? __funnelshift_r(w, w, 12) : w >> (4 * I));
+  return (x & kCode) | kBase;
+}
+// Operand pairs of a V word: channel i of both tokens.
+template <int I>
+__device__ __forceinline__ uint32_t v_pair(uint32_t w) {
+  const uint32_t x = I == 0 ? w << 3 : w >> (4 * I - 3);
+  return (x & kCode) | kBase;
+}
 
 template <int D>
-__global__ void __launch_bounds__(32 * kWarps) decode_q4_kernel(const DecodeQ4Launch a) {
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[D / 32]) {
+  if constexpr (D == 128) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x;
+    w[1] = v.y;
+  }
+}
+// The G bf16 scales of a token as fp32.
+template <int D>
+__device__ __forceinline__ void load_scales(const uint8_t* p, float (&s)[D / 32]) {
+  if constexpr (D == 128) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    s[0] = bf16lo_to_f32(v.x);
+    s[1] = bf16hi_to_f32(v.x);
+    s[2] = bf16lo_to_f32(v.y);
+    s[3] = bf16hi_to_f32(v.y);
+  } else {
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
+    s[0] = bf16lo_to_f32(v);
+    s[1] = bf16hi_to_f32(v);
+  }
+}
+
+// First record of CTA c's range, and the CTA of a record, for R records in N ranges.
+__device__ __forceinline__ long long range_of(long long R, int N, int c) { return R * c / N; }
+__device__ __forceinline__ int cta_of(long long R, int N, long long x) {
+  return static_cast<int>(((x + 1) * N - 1) / R);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const DecodeQ4Launch a) {
   using L = Q4Layout<D>;
-  constexpr int C = D / 32;
-  __shared__ float sm_m[kWarps][kMaxG], sm_l[kWarps][kMaxG], sm_o[kWarps][kMaxG][D];
-  const int g = blockIdx.x, b = blockIdx.y;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int G = a.Hq / a.Hkv;
+  using S = Q4Smem<D>;
+  constexpr int NT = S::NT, GR = L::G;
+  extern __shared__ __align__(128) uint8_t smem[];
+  float4* sm_acc = reinterpret_cast<float4*>(smem + S::RING);
+  float* sm_m = reinterpret_cast<float*>(smem + S::ML);
+  float* sm_l = sm_m + kWarps * 8;
+  float* sm_fm = reinterpret_cast<float*>(smem + S::FIN);       // [8] reference, then
+  float* sm_fl = sm_fm + 8;                                     // [8] sum of the merged row
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::BAR);
+  uint64_t* empty = full + kStages;
+  int* flag = reinterpret_cast<int*>(smem + S::FLAG);
+  long long* sm_total = reinterpret_cast<long long*>(smem + S::MISC);        // [0] R, [1] row0 of the start
+  int* sm_start = reinterpret_cast<int*>(smem + S::MISC + 16);               // b of the start
+  int* sm_ticket = sm_start + 1;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  if (tid < kStages) {
+    mbar_init(full + tid, 1);
+    mbar_init(empty + tid, 1);
+  }
+  fence_barrier_init();
+  griddep_launch_dependents();
+  griddep_wait();
+
   const bool fa = a.layer_mode == nullptr || a.layer_mode[a.layer] != 0;
-  const size_t row0 = static_cast<size_t>(b) * a.Hq + g * G;
-  int s = a.seqlens[b];
-  if (s < 0 || s > static_cast<long long>(a.max_pages) * a.page_size) {
-    if (g == 0 && threadIdx.x == 0) raise_error(a.st.err, DEV_ERR_SEQLEN);
-    s = 0;
-  }
-  const int nb = s > 0 ? (s - 1) / a.block + 1 : 0;
-  const int n_sink = fa ? s : static_cast<int>(min(static_cast<long long>(a.sink_blocks) * a.block,
-                                                   static_cast<long long>(s)));
-  const int win = fa ? 0 : max(0, nb - a.window_blocks) * a.block;
-  float q[kMaxG][C], o[kMaxG][C], m[kMaxG], l[kMaxG];
-  for (int h = 0; h < kMaxG; ++h) {
-    m[h] = -INFINITY;
-    l[h] = 0.f;
-    for (int c = 0; c < C; ++c) {
-      o[h][c] = 0.f;
-      q[h][c] = h < G ? __uint_as_float(static_cast<uint32_t>(a.q[(row0 + h) * D + lane * C + c]) << 16)
-                      : 0.f;
-    }
-  }
-  const float sl2 = a.scale * 1.4426950408889634f;
-  const int recs = a.page_size / kQ4Rec;
-  for (int rr = warp; rr < (s + kQ4Rec - 1) / kQ4Rec; rr += kWarps) {
-    const int u0 = rr * kQ4Rec;
-    if (u0 >= n_sink && u0 + kQ4Rec <= win) continue;
-    const int page = a.page_table[static_cast<size_t>(b) * a.max_pages + u0 / a.page_size];
-    if (page < 0 || page >= a.num_pages) {
-      if (lane == 0) raise_error(a.st.err, DEV_ERR_PAGE);
-      continue;
-    }
-    const uint8_t* rec = a.pool + ((static_cast<size_t>(page) * a.Hkv + g) * recs +
-                                   u0 % a.page_size / kQ4Rec) * L::BYTES;
-    for (int r = 0; r < kQ4Rec; ++r) {
-      const int u = u0 + r;
-      if (u >= s || !(u < n_sink || u >= win)) continue;
-      float k[C], v[C];
-      for (int c = 0; c < C; ++c) {
-        const int ch = lane * C + c, w = ch / 32, t = ch % 32 / 8, e = ch % 8;
-        uint32_t word = *reinterpret_cast<const uint32_t*>(rec + r * (D / 2) + t * (D / 8) + 4 * w);
-        word = __funnelshift_r(word, word, 3);
-        const int nk = static_cast<int>((word >> (16 * (e & 1) + 4 * (e >> 1))) & 15) - 8;
-        const int gv = ch / (D / 8), j = ch % (D / 8) / 4, i = ch % 4;
-        const uint32_t half = *reinterpret_cast<const uint16_t*>(
-            rec + L::VC + (r / 8) * 4 * D + (4 * gv + r % 8 / 2) * (D / 8) + 4 * j + 2 * (r & 1));
-        const int nv = static_cast<int>((half >> (4 * i)) & 15) - 8;
-        k[c] = nk * __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(
-                        rec + L::KS)[r * L::G + w]) << 16);
-        v[c] = nv * __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(
-                        rec + L::VS)[w * 16 + r]) << 16);
-      }
+  const int G = a.Hq / a.Hkv;
+
+  // ---- records of all rows, and where this CTA's range starts -------------
+  // Thread t owns `per` consecutive sequences; a block scan of their records.
+  const int per = (a.B + kThreads - 1) / kThreads;
+  const int bt0 = tid * per, bt1 = min(bt0 + per, a.B);
+  long long mine = 0;
+  for (int b = bt0; b < bt1; ++b) mine += live_of(a, b, fa).count;
+  mine *= a.Hkv;
+  long long incl = mine;
 #pragma unroll
-      for (int h = 0; h < kMaxG; ++h) {
-        if (h >= G) break;
-        float x = 0.f;
-        for (int c = 0; c < C; ++c) x += q[h][c] * k[c];
-        for (int st = 16; st > 0; st >>= 1) x += __shfl_xor_sync(0xffffffffu, x, st);
-        x *= sl2;
-        const float mn = fmaxf(m[h], x);
-        const float mu = mn == -INFINITY ? 0.f : mn;
-        const float alpha = exp2f(m[h] - mu), p = exp2f(x - mu);
-        m[h] = mn;
-        l[h] = l[h] * alpha + p;
-        for (int c = 0; c < C; ++c) o[h][c] = o[h][c] * alpha + p * v[c];
-      }
-    }
+  for (int s = 1; s < 32; s <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, incl, s);
+    if (lane >= s) incl += x;
   }
-  for (int h = 0; h < kMaxG; ++h) {
-    if (lane == 0) {
-      sm_m[warp][h] = m[h];
-      sm_l[warp][h] = l[h];
+  long long* wsum = reinterpret_cast<long long*>(sm_acc);        // [kThreads / 32]
+  if (lane == 31) wsum[warp] = incl;
+  __syncthreads();
+  long long before = incl - mine, R = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const long long x = wsum[w];
+    if (w < warp) before += x;
+    R += x;
+  }
+  // At least one record per consumer warp before another CTA joins in.
+  const int N = static_cast<int>(min(static_cast<long long>(gridDim.x), (R + kWarps - 1) / kWarps));
+  const int cta = blockIdx.x;
+  const bool works = cta < N;
+  const long long R0 = works ? range_of(R, N, cta) : 0, R1 = works ? range_of(R, N, cta + 1) : 0;
+  if (works && R0 >= before && R0 < before + mine) {             // one thread
+    long long at = before;
+    int b = bt0;
+    for (;; ++b) {
+      const long long n = static_cast<long long>(live_of(a, b, fa).count) * a.Hkv;
+      if (R0 < at + n) break;
+      at += n;
     }
-    for (int c = 0; c < C; ++c) sm_o[warp][h][lane * C + c] = o[h][c];
+    *sm_start = b;
+    sm_total[1] = at;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < G * D; i += 32 * kWarps) {
-    const int h = i / D, c = i % D;
-    float M = -INFINITY, ls = 0.f, O = 0.f;
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w][h]);
-    const float mu = M == -INFINITY ? 0.f : M;
-    for (int w = 0; w < kWarps; ++w) {
-      const float wt = exp2f(sm_m[w][h] - mu);
-      ls += wt * sm_l[w][h];
-      O += wt * sm_o[w][h][c];
+
+  if (warp == kWarps) {
+    // ---- producer ----------------------------------------------------------
+    if (works && lane < kStages) {
+      Walk w;
+      w.b = *sm_start;
+      w.v = live_of(a, w.b, fa);
+      const long long at = sm_total[1];
+      w.g = static_cast<int>((R0 - at) / w.v.count);
+      w.row0 = at + static_cast<long long>(w.g) * w.v.count;
+      const int recs = a.page_size / kQ4Rec;
+      uint8_t* dst = smem + lane * L::BYTES;
+      uint32_t it = 0;
+      bool ok = true;
+      for (long long x = R0 + lane; x < R1 && ok; x += kStages, ++it) {
+        while (x >= w.row0 + w.v.count) next_row(a, fa, w);
+        const int k = static_cast<int>(x - w.row0);
+        const int rec = k < w.v.head ? k : w.v.tail + (k - w.v.head);
+        const int lp = rec / recs;
+        const int page = a.page_table[static_cast<size_t>(w.b) * a.max_pages + lp];
+        if (it > 0 && !mbar_drain(empty + lane, (it - 1) & 1, a.st.spin_ns)) {
+          raise_error(a.st.err, DEV_ERR_TIMEOUT);
+          ok = false;
+          break;
+        }
+        const bool good = page >= 0 && page < a.num_pages;
+        flag[lane] = good;
+        if (good) {
+          mbar_arrive_expect_tx(full + lane, L::BYTES);
+          bulk_load(dst,
+                    a.pool + ((static_cast<size_t>(page) * a.Hkv + w.g) * recs + (rec - lp * recs)) * L::BYTES,
+                    L::BYTES, full + lane);
+        } else {
+          raise_error(a.st.err, DEV_ERR_PAGE);
+          mbar_arrive(full + lane);
+        }
+      }
+      // The last copy into this lane's stage has landed before the CTA may end.
+      if (it > 0) mbar_drain(full + lane, (it - 1) & 1);
     }
-    const float out = ls != 0.f ? O / ls : 0.f;
-    a.o[(row0 + h) * D + c] = __bfloat16_as_ushort(__float2bfloat16_rn(out));
-    if (c == 0 && a.lse)
-      a.lse[row0 + h] = ls != 0.f ? (M + log2f(ls)) * 0.69314718055994531f : -INFINITY;
+    return;
   }
+
+  // ---- consumers -------------------------------------------------------------
+  const int g = lane >> 2, t = lane & 3;
+  constexpr int kConsumers = 32 * kWarps;
+
+  // Sequences with no live token: zero output, lse -inf.
+  for (int b = cta; b < a.B; b += gridDim.x) {
+    if (live_of(a, b, fa).count != 0) continue;
+    if (tid == 0) {
+      const int s = a.seqlens[b];
+      if (s < 0 || s > static_cast<long long>(a.max_pages) * a.page_size)
+        raise_error(a.st.err, DEV_ERR_SEQLEN);
+    }
+    uint32_t* o = reinterpret_cast<uint32_t*>(a.o + static_cast<size_t>(b) * a.Hq * D);
+    for (int i = tid; i < a.Hq * (D / 2); i += kConsumers) o[i] = 0;
+    if (a.lse)
+      for (int i = tid; i < a.Hq; i += kConsumers) a.lse[static_cast<size_t>(b) * a.Hq + i] = -INFINITY;
+  }
+  if (!works) return;
+
+  const float sl2 = a.scale * 1.4426950408889634f, inv_sl2 = 1.f / sl2;
+  Walk w;
+  w.b = *sm_start;
+  w.v = live_of(a, w.b, fa);
+  {
+    const long long at = sm_total[1];
+    w.g = static_cast<int>((R0 - at) / w.v.count);
+    w.row0 = at + static_cast<long long>(w.g) * w.v.count;
+  }
+  bool ok = true;
+  uint32_t taken = 0;                                            // records this warp has had
+  float4* part = reinterpret_cast<float4*>(a.part);              // [2 gridDim][PART4], then m, l [..][8]
+  float* part_m = a.part + static_cast<size_t>(2) * gridDim.x * S::PART4 * 4;
+  float* part_l = part_m + 2 * gridDim.x * 8;
+
+  for (long long at = R0; at < R1;) {
+    const long long row1 = w.row0 + w.v.count;
+    const long long end = min(row1, R1);
+    const size_t head0 = static_cast<size_t>(w.b) * a.Hq + w.g * G;   // the group's first query head
+
+    // Query operands: lane 4 g + t holds head g, channels 32 w + 8 t + e; and
+    // -24 times the group sums of heads 2 t and 2 t + 1.
+    uint32_t qf[GR][4];
+    float c0[GR], c1[GR];
+#pragma unroll
+    for (int i = 0; i < GR; ++i) {
+      uint4 v = {0, 0, 0, 0};
+      if (g < G) v = *reinterpret_cast<const uint4*>(a.q + (head0 + g) * D + 32 * i + 8 * t);
+      qf[i][0] = v.x;
+      qf[i][1] = v.y;
+      qf[i][2] = v.z;
+      qf[i][3] = v.w;
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum += bf16lo_to_f32(qf[i][e]) + bf16hi_to_f32(qf[i][e]);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      c0[i] = -24.f * __shfl_sync(0xffffffffu, sum, 8 * t);
+      c1[i] = -24.f * __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+    }
+
+    float o[NT][4];
+#pragma unroll
+    for (int m = 0; m < NT; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
+    float l0 = 0.f, l1 = 0.f;
+    float m0 = kLowest, m1 = kLowest;          // softmax references (log2 units) of heads 2 t, 2 t + 1
+    float th0 = kLowest, th1 = kLowest;        // a score (before the scale) above it moves the reference
+
+    // The warp takes every kWarps-th record of the CTA's range.
+    const int skip = (warp + kWarps - static_cast<int>((at - R0) % kWarps)) % kWarps;
+    const int k_end = static_cast<int>(end - w.row0);
+    for (int k = static_cast<int>(at - w.row0) + skip; k < k_end; k += kWarps, ++taken) {
+      const int stage = warp + kWarps * static_cast<int>(taken & (kDepth - 1));
+      if (ok) ok = mbar_drain(full + stage, (taken / kDepth) & 1, a.st.spin_ns);
+      if (!__all_sync(0xffffffffu, ok)) {
+        if (lane == 0) raise_error(a.st.err, DEV_ERR_TIMEOUT);
+        ok = false;
+        continue;
+      }
+      const uint8_t* rec = smem + stage * L::BYTES;
+      const int u0 = (k < w.v.head ? k : w.v.tail + (k - w.v.head)) * kQ4Rec;
+      if (flag[stage] == 0) {                  // no such page
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty + stage);
+        continue;
+      }
+      uint32_t k0[GR], k1[GR], v0[GR], v1[GR];
+      float s0[GR], s1[GR];
+      load_words<D>(rec + lane * (D / 8), k0);
+      load_words<D>(rec + 4 * D + lane * (D / 8), k1);
+      load_scales<D>(rec + L::KS + g * (2 * GR), s0);
+      load_scales<D>(rec + L::KS + (g + 8) * (2 * GR), s1);
+
+      float x00 = 0.f, x01 = 0.f, x10 = 0.f, x11 = 0.f;
+#pragma unroll
+      for (int i = 0; i < GR; ++i) {
+        float acc[4];
+        {
+          const uint32_t af[4] = {k_pair<0>(k0[i]), k_pair<0>(k1[i]), k_pair<1>(k0[i]), k_pair<1>(k1[i])};
+          mma_first(acc, af, qf[i][0], qf[i][1], c0[i], c1[i]);
+        }
+        {
+          const uint32_t af[4] = {k_pair<2>(k0[i]), k_pair<2>(k1[i]), k_pair<3>(k0[i]), k_pair<3>(k1[i])};
+          mma_bf16_16816(acc, af, qf[i][2], qf[i][3]);
+        }
+        x00 = fmaf(s0[i], acc[0], x00);
+        x01 = fmaf(s0[i], acc[1], x01);
+        x10 = fmaf(s1[i], acc[2], x10);
+        x11 = fmaf(s1[i], acc[3], x11);
+      }
+      load_words<D>(rec + L::VC + lane * (D / 8), v0);
+      load_words<D>(rec + L::VC + 4 * D + lane * (D / 8), v1);
+      const uint8_t* vs = rec + L::VS + (g * (D / 8) / 32) * 32 + 4 * t;
+      uint32_t sv0 = *reinterpret_cast<const uint32_t*>(vs);
+      uint32_t sv1 = *reinterpret_cast<const uint32_t*>(vs + 16);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + stage);
+      // A record at the end of the sequence or of the sink or window: tokens
+      // that are not live score -inf, and their values count as zero whatever
+      // bytes stand there.
+      if (!(w.v.s - u0 >= kQ4Rec && (w.v.n_sink - u0 >= kQ4Rec || u0 >= w.v.win))) {
+        auto live = [&](int u) { return u < w.v.s && (u < w.v.n_sink || u >= w.v.win); };
+        if (!live(u0 + g)) x00 = x01 = -INFINITY;
+        if (!live(u0 + g + 8)) x10 = x11 = -INFINITY;
+        if (!live(u0 + 2 * t)) sv0 &= 0xffff0000u;
+        if (!live(u0 + 2 * t + 1)) sv0 &= 0x0000ffffu;
+        if (!live(u0 + 2 * t + 8)) sv1 &= 0xffff0000u;
+        if (!live(u0 + 2 * t + 9)) sv1 &= 0x0000ffffu;
+      }
+      const float t0 = fmaxf(x00, x10), t1 = fmaxf(x01, x11);
+      if (__any_sync(0xffffffffu, t0 > th0 || t1 > th1)) {
+        float n0 = t0, n1 = t1;
+#pragma unroll
+        for (int s = 4; s < 32; s <<= 1) {
+          n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, s));
+          n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, s));
+        }
+        n0 = fmaxf(m0, n0 * sl2);
+        n1 = fmaxf(m1, n1 * sl2);
+        const float f0 = ex2(m0 - n0), f1 = ex2(m1 - n1);
+        m0 = n0;
+        m1 = n1;
+        th0 = (n0 + kGrow) * inv_sl2;
+        th1 = (n1 + kGrow) * inv_sl2;
+        l0 *= f0;
+        l1 *= f1;
+#pragma unroll
+        for (int m = 0; m < NT; ++m) {
+          o[m][0] *= f0;
+          o[m][1] *= f1;
+          o[m][2] *= f0;
+          o[m][3] *= f1;
+        }
+      }
+      const float p00 = ex2(fmaf(x00, sl2, -m0)), p01 = ex2(fmaf(x01, sl2, -m1));
+      const float p10 = ex2(fmaf(x10, sl2, -m0)), p11 = ex2(fmaf(x11, sl2, -m1));
+      l0 += p00 + p10;
+      l1 += p01 + p11;
+      const uint32_t b0 = movmatrix_trans(pack_bf16x2(p00, p01));
+      const uint32_t b1 = movmatrix_trans(pack_bf16x2(p10, p11));
+      // -24 s (exact: 5 bits times 3)
+      const uint32_t n0 = fma_bf16x2(sv0, 0xc1c0c1c0u, 0u), n1 = fma_bf16x2(sv1, 0xc1c0c1c0u, 0u);
+#pragma unroll
+      for (int j = 0; j < GR; ++j) {
+        {
+          const uint32_t af[4] = {fma_bf16x2(v_pair<0>(v0[j]), sv0, n0), fma_bf16x2(v_pair<1>(v0[j]), sv0, n0),
+                                  fma_bf16x2(v_pair<0>(v1[j]), sv1, n1), fma_bf16x2(v_pair<1>(v1[j]), sv1, n1)};
+          mma_bf16_16816(o[2 * j], af, b0, b1);
+        }
+        {
+          const uint32_t af[4] = {fma_bf16x2(v_pair<2>(v0[j]), sv0, n0), fma_bf16x2(v_pair<3>(v0[j]), sv0, n0),
+                                  fma_bf16x2(v_pair<2>(v1[j]), sv1, n1), fma_bf16x2(v_pair<3>(v1[j]), sv1, n1)};
+          mma_bf16_16816(o[2 * j + 1], af, b0, b1);
+        }
+      }
+    }
+
+    // ---- merge the warps --------------------------------------------------
+#pragma unroll
+    for (int s = 4; s < 32; s <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, s);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, s);
+    }
+#pragma unroll
+    for (int m = 0; m < NT; ++m)
+      sm_acc[warp * S::PART4 + m * 32 + lane] = make_float4(o[m][0], o[m][1], o[m][2], o[m][3]);
+    if (g == 0) {
+      sm_m[warp * 8 + 2 * t] = m0;
+      sm_m[warp * 8 + 2 * t + 1] = m1;
+      sm_l[warp * 8 + 2 * t] = l0;
+      sm_l[warp * 8 + 2 * t + 1] = l1;
+    }
+    const bool fine = named_bar_and(1, kConsumers, ok);
+    const bool whole = at == w.row0 && end == row1;
+    const int slot = 2 * cta + (at == w.row0 ? 1 : 0);
+    for (int i = tid; i < S::PART4; i += kConsumers) {
+      const int h = 2 * (i & 3), gi = (i & 31) >> 2, m = i >> 5;
+      if (h >= G) continue;
+      float M0 = kLowest, M1 = kLowest;
+#pragma unroll
+      for (int v = 0; v < kWarps; ++v) {
+        M0 = fmaxf(M0, sm_m[v * 8 + h]);
+        M1 = fmaxf(M1, sm_m[v * 8 + h + 1]);
+      }
+      float ls0 = 0.f, ls1 = 0.f;
+      float4 r = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int v = 0; v < kWarps; ++v) {
+        const float w0 = ex2(sm_m[v * 8 + h] - M0), w1 = ex2(sm_m[v * 8 + h + 1] - M1);
+        const float4 c = sm_acc[v * S::PART4 + i];
+        ls0 = fmaf(w0, sm_l[v * 8 + h], ls0);
+        ls1 = fmaf(w1, sm_l[v * 8 + h + 1], ls1);
+        r.x = fmaf(w0, c.x, r.x);
+        r.y = fmaf(w1, c.y, r.y);
+        r.z = fmaf(w0, c.z, r.z);
+        r.w = fmaf(w1, c.w, r.w);
+      }
+      if (!fine) {                             // a wait ran out: the row's output is zero
+        ls0 = ls1 = whole ? 0.f : -1.f;
+        r = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      if (whole) {
+        const float i0 = ls0 != 0.f ? 1.f / ls0 : 0.f, i1 = ls1 != 0.f ? 1.f / ls1 : 0.f;
+        uint16_t* out = a.o + (head0 + h) * D + gi * (D / 8) + 2 * m;
+        *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(r.x * i0, r.z * i0);
+        if (h + 1 < G) *reinterpret_cast<uint32_t*>(out + D) = pack_bf16x2(r.y * i1, r.w * i1);
+        if (a.lse && m == 0 && gi == 0) {
+          a.lse[head0 + h] = ls0 != 0.f ? (M0 + log2f(ls0)) * 0.69314718055994531f : -INFINITY;
+          if (h + 1 < G) a.lse[head0 + h + 1] = ls1 != 0.f ? (M1 + log2f(ls1)) * 0.69314718055994531f : -INFINITY;
+        }
+      } else {
+        __stcg(part + static_cast<size_t>(slot) * S::PART4 + i, r);
+        if (m == 0 && gi == 0) {
+          __stcg(part_m + slot * 8 + h, M0);
+          __stcg(part_m + slot * 8 + h + 1, M1);
+          __stcg(part_l + slot * 8 + h, ls0);
+          __stcg(part_l + slot * 8 + h + 1, ls1);
+        }
+      }
+    }
+    if (!whole) {
+      // ---- merge the CTAs of a row: the one that comes last ----------------
+      const int first = cta_of(R, N, w.row0), last = cta_of(R, N, row1 - 1);
+      __threadfence();
+      named_bar_sync(1, kConsumers);
+      if (tid == 0) {
+        int* ticket = a.tickets + static_cast<size_t>(w.b) * a.Hkv + w.g;
+        const int n = atomicAdd(ticket, 1);
+        *sm_ticket = n;
+        if (n == last - first) *ticket = 0;
+        __threadfence();
+      }
+      named_bar_sync(1, kConsumers);
+      if (*sm_ticket == last - first) {
+        __threadfence();
+        // slot of part c: the first CTA's row begins there, the others' before
+        const int f0 = 2 * first + 1;
+        float* wt = reinterpret_cast<float*>(sm_acc);              // [part][8] weights
+        const int np = last - first + 1;
+        for (int i = tid; i < 8 * np; i += kConsumers) {
+          const int c = i >> 3, h = i & 7;
+          const int sl = c == 0 ? f0 : 2 * (first + c);
+          wt[i] = h < G ? __ldcg(part_m + sl * 8 + h) : kLowest;
+        }
+        named_bar_sync(1, kConsumers);
+        if (tid < 8) {
+          float M = kLowest;
+          for (int c = 0; c < np; ++c) M = fmaxf(M, wt[c * 8 + tid]);
+          sm_fm[tid] = M;
+        }
+        named_bar_sync(1, kConsumers);
+        for (int i = tid; i < 8 * np; i += kConsumers) {
+          wt[i] = ex2(wt[i] - sm_fm[i & 7]);
+        }
+        named_bar_sync(1, kConsumers);
+        if (tid < 8 && tid < G) {
+          float ls = 0.f;
+          bool lost = false;
+          for (int c = 0; c < np; ++c) {
+            const float l = __ldcg(part_l + (c == 0 ? f0 : 2 * (first + c)) * 8 + tid);
+            lost |= l < 0.f;
+            ls = fmaf(wt[c * 8 + tid], l, ls);
+          }
+          if (lost) ls = 0.f;
+          sm_fl[tid] = ls != 0.f ? 1.f / ls : 0.f;
+          if (a.lse)
+            a.lse[head0 + tid] = ls != 0.f ? (sm_fm[tid] + log2f(ls)) * 0.69314718055994531f : -INFINITY;
+        }
+        named_bar_sync(1, kConsumers);
+        for (int i = tid; i < S::PART4; i += kConsumers) {
+          const int h = 2 * (i & 3), gi = (i & 31) >> 2, m = i >> 5;
+          if (h >= G) continue;
+          float4 r = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+          for (int c = 0; c < np; ++c) {
+            const float4 v = __ldcg(part + static_cast<size_t>(c == 0 ? f0 : 2 * (first + c)) * S::PART4 + i);
+            const float w0 = wt[c * 8 + h], w1 = wt[c * 8 + h + 1];
+            r.x = fmaf(w0, v.x, r.x);
+            r.y = fmaf(w1, v.y, r.y);
+            r.z = fmaf(w0, v.z, r.z);
+            r.w = fmaf(w1, v.w, r.w);
+          }
+          const float i0 = sm_fl[h], i1 = sm_fl[h + 1];
+          uint16_t* out = a.o + (head0 + h) * D + gi * (D / 8) + 2 * m;
+          *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(r.x * i0, r.z * i0);
+          if (h + 1 < G) *reinterpret_cast<uint32_t*>(out + D) = pack_bf16x2(r.y * i1, r.w * i1);
+        }
+      }
+    }
+    at = end;
+    if (at < R1) {
+      next_row(a, fa, w);
+      named_bar_sync(1, kConsumers);      // the merge buffer is free again
+    }
+  }
+}
+
+template <int D>
+cudaError_t launch_t(const DecodeQ4Launch& p, int num_sms, cudaStream_t stream) {
+  constexpr int smem = Q4Smem<D>::BYTES;
+  cudaError_t e = cudaFuncSetAttribute(decode_q4_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kCtasPerSm * num_sms);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_q4_kernel<D>, p);
 }
 
 }  // namespace
 
+// Two partials per CTA: float4 accumulators, m and l of 8 heads.
 size_t decode_q4_workspace_bytes(int d, int num_sms) {
-  (void)d;
-  (void)num_sms;
-  return 0;
+  const size_t parts = static_cast<size_t>(2) * kCtasPerSm * num_sms;
+  return parts * (static_cast<size_t>(d) / 16 * 32 * 16 + 2 * 8 * 4);
 }
 
 cudaError_t launch_decode_q4(const DecodeQ4Launch& p, int num_sms, cudaStream_t stream) {
-  (void)num_sms;
-  const dim3 grid(p.Hkv, p.B);
-  if (p.d == 64) decode_q4_kernel<64><<<grid, 32 * kWarps, 0, stream>>>(p);
-  else decode_q4_kernel<128><<<grid, 32 * kWarps, 0, stream>>>(p);
-  return cudaGetLastError();
+  return p.d == 64 ? launch_t<64>(p, num_sms, stream) : launch_t<128>(p, num_sms, stream);
 }
 
 }  // namespace flux
