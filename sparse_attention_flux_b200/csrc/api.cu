@@ -905,6 +905,8 @@ extern "C" int flux_attn_decode_q4(flux_ctx* c, const uint16_t* q, const uint8_t
   if (static_cast<long long>(B) * Hkv > kMaxTickets)
     return fail(FLUX_ERR_SHAPE, "%s: B * Hkv = %lld exceeds %d", name,
                 static_cast<long long>(B) * Hkv, kMaxTickets);
+  if (static_cast<double>(num_pages) * Hkv * (page_size / 16) >= 4294967295.0)
+    return fail(FLUX_ERR_SHAPE, "%s: the cache has 2^32 records or more", name);
   if (!aligned16(q) || !aligned16(o))
     return fail(FLUX_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", name);
   if ((rc = check_device(c, name)) != FLUX_OK) return rc;

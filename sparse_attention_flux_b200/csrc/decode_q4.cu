@@ -9,15 +9,17 @@
 // Work split.  The live records of all (sequence, kv head) rows are laid end to
 // end and cut into equal ranges, one per CTA (two CTAs per SM, one wave), so a
 // ragged batch loads every SM alike.  A CTA walks its range row by row; within
-// a row its consumer warps take records in turn and merge at the row's
+// a row its warps take records in turn and merge at the row's
 // end in shared memory.  A row that crosses a range border (at most the first
 // and the last of a CTA) leaves a partial in the workspace; the CTA that
 // delivers a row's last partial (a ticket) merges them in range order, so the
 // result does not depend on timing.
 //
-// Stream.  A producer warp walks the same range ahead of the consumers, one
-// lane per ring stage: it looks up the record's page and copies the record (one
-// contiguous bulk copy) into shared memory, 28 records in flight per CTA.
+// Stream.  Each warp keeps a ring of four records in shared memory, filled by
+// bulk copies (a record is one contiguous copy): when the warp has taken a
+// record's operands into registers it refills the stage itself, so a full
+// barrier per stage is all the synchronisation there is.  The places of a
+// warp's next 32 records are looked up at once, a lane each.
 //
 // Arithmetic per record, one warp, warp MMAs (m16n8k16, bf16, fp32 sums):
 //   S = K q^T: the 16 tokens are the rows, the group's query heads (up to 8)
@@ -37,14 +39,11 @@ namespace flux {
 
 namespace {
 
-constexpr int kWarps = 7;                   // consumer warps: with the producer 16 warps per SM, 128
-                                            // registers each (8 + 1 would leave 96, and spills)
-constexpr int kThreads = 32 * kWarps + 32;  // + the producer warp
-constexpr int kDepth = 4;                   // ring stages per warp
-constexpr int kStages = kDepth * kWarps;    // records in flight per CTA, a producer lane each.  A stage
-                                            // belongs to one warp: a wait tells only the parity of a
-                                            // phase, so no other may come to it a round early
-static_assert(kStages <= 32 && (kDepth & (kDepth - 1)) == 0, "one producer lane per stage");
+constexpr int kWarps = 8;                   // per CTA; 16 per SM, 128 registers a thread
+constexpr int kThreads = 32 * kWarps;
+constexpr int kDepth = 4;                   // ring stages of a warp
+constexpr int kStages = kDepth * kWarps;
+constexpr uint32_t kNoRecord = 0xffffffffu;
 constexpr int kCtasPerSm = 2;
 constexpr float kGrow = 8.f;                // log2 growth of a score that is tolerated
 constexpr float kLowest = -3.0e38f;         // reference of a row without tokens: finite, so that
@@ -61,8 +60,7 @@ struct Q4Smem {
   static constexpr int ML = RING + ACC;                   // m, l [warp][8]
   static constexpr int FIN = ML + 2 * kWarps * 8 * 4;     // weights and 1 / l of the final merge
   static constexpr int BAR = FIN + 2 * 8 * 4;
-  static constexpr int FLAG = BAR + 2 * kStages * 8;
-  static constexpr int MISC = FLAG + kStages * 4;         // start row, totals, ticket
+  static constexpr int MISC = BAR + kStages * 8;          // start row, totals, ticket
   static constexpr int BYTES = MISC + 64;
 };
 
@@ -146,20 +144,30 @@ __device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4],
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
 
-constexpr uint32_t kCode = 0x00780078u;     // the upper four mantissa bits of both halves
-constexpr uint32_t kBase = 0x41804180u;     // 16.0, 16.0
-
+// (x & code) | base with both constants in registers: one LOP3.
+struct Unpack {
+  uint32_t code, base;
+};
+__device__ __forceinline__ Unpack unpack_masks() {
+  Unpack u;             // opaque to the compiler, which would fold them into two instructions
+  asm volatile("mov.u32 %0, 0x00780078;" : "=r"(u.code));   // the upper four mantissa bits of both halves
+  asm volatile("mov.u32 %0, 0x41804180;" : "=r"(u.base));   // 16.0, 16.0
+  return u;
+}
+__device__ __forceinline__ uint32_t and_or(uint32_t x, const Unpack& u) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(u.code), "r"(u.base));
+  return r;
+}
 // Operand pairs of a K word (stored rotated left by 3): channels 2 i, 2 i + 1.
 template <int I>
-__device__ __forceinline__ uint32_t k_pair(uint32_t w) {
-  const uint32_t x = I == 0 ? w : (I == 3 ? __funnelshift_r(w, w, 12) : w >> (4 * I));
-  return (x & kCode) | kBase;
+__device__ __forceinline__ uint32_t k_pair(uint32_t w, const Unpack& u) {
+  return and_or(I == 0 ? w : (I == 3 ? __funnelshift_r(w, w, 12) : w >> (4 * I)), u);
 }
 // Operand pairs of a V word: channel i of both tokens.
 template <int I>
-__device__ __forceinline__ uint32_t v_pair(uint32_t w) {
-  const uint32_t x = I == 0 ? w << 3 : w >> (4 * I - 3);
-  return (x & kCode) | kBase;
+__device__ __forceinline__ uint32_t v_pair(uint32_t w, const Unpack& u) {
+  return and_or(I == 0 ? w << 3 : w >> (4 * I - 3), u);
 }
 
 template <int D>
@@ -210,17 +218,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
   float* sm_fm = reinterpret_cast<float*>(smem + S::FIN);       // [8] reference, then
   float* sm_fl = sm_fm + 8;                                     // [8] sum of the merged row
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::BAR);
-  uint64_t* empty = full + kStages;
-  int* flag = reinterpret_cast<int*>(smem + S::FLAG);
   long long* sm_total = reinterpret_cast<long long*>(smem + S::MISC);        // [0] R, [1] row0 of the start
   int* sm_start = reinterpret_cast<int*>(smem + S::MISC + 16);               // b of the start
   int* sm_ticket = sm_start + 1;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-  if (tid < kStages) {
-    mbar_init(full + tid, 1);
-    mbar_init(empty + tid, 1);
-  }
+  if (tid < kStages) mbar_init(full + tid, 1);
   fence_barrier_init();
   griddep_launch_dependents();
   griddep_wait();
@@ -241,17 +244,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
     const long long x = __shfl_up_sync(0xffffffffu, incl, s);
     if (lane >= s) incl += x;
   }
-  long long* wsum = reinterpret_cast<long long*>(sm_acc);        // [kThreads / 32]
+  long long* wsum = reinterpret_cast<long long*>(sm_acc);        // [kWarps]
   if (lane == 31) wsum[warp] = incl;
   __syncthreads();
   long long before = incl - mine, R = 0;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
+  for (int w = 0; w < kWarps; ++w) {
     const long long x = wsum[w];
     if (w < warp) before += x;
     R += x;
   }
-  // At least one record per consumer warp before another CTA joins in.
+  // At least one record per warp before another CTA joins in.
   const int N = static_cast<int>(min(static_cast<long long>(gridDim.x), (R + kWarps - 1) / kWarps));
   const int cta = blockIdx.x;
   const bool works = cta < N;
@@ -269,51 +272,60 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
   }
   __syncthreads();
 
-  if (warp == kWarps) {
-    // ---- producer ----------------------------------------------------------
-    if (works && lane < kStages) {
-      Walk w;
-      w.b = *sm_start;
-      w.v = live_of(a, w.b, fa);
-      const long long at = sm_total[1];
-      w.g = static_cast<int>((R0 - at) / w.v.count);
-      w.row0 = at + static_cast<long long>(w.g) * w.v.count;
-      const int recs = a.page_size / kQ4Rec;
-      uint8_t* dst = smem + lane * L::BYTES;
-      uint32_t it = 0;
-      bool ok = true;
-      for (long long x = R0 + lane; x < R1 && ok; x += kStages, ++it) {
-        while (x >= w.row0 + w.v.count) next_row(a, fa, w);
-        const int k = static_cast<int>(x - w.row0);
-        const int rec = k < w.v.head ? k : w.v.tail + (k - w.v.head);
-        const int lp = rec / recs;
-        const int page = a.page_table[static_cast<size_t>(w.b) * a.max_pages + lp];
-        if (it > 0 && !mbar_drain(empty + lane, (it - 1) & 1, a.st.spin_ns)) {
-          raise_error(a.st.err, DEV_ERR_TIMEOUT);
-          ok = false;
-          break;
-        }
-        const bool good = page >= 0 && page < a.num_pages;
-        flag[lane] = good;
-        if (good) {
-          mbar_arrive_expect_tx(full + lane, L::BYTES);
-          bulk_load(dst,
-                    a.pool + ((static_cast<size_t>(page) * a.Hkv + w.g) * recs + (rec - lp * recs)) * L::BYTES,
-                    L::BYTES, full + lane);
-        } else {
-          raise_error(a.st.err, DEV_ERR_PAGE);
-          mbar_arrive(full + lane);
-        }
-      }
-      // The last copy into this lane's stage has landed before the CTA may end.
-      if (it > 0) mbar_drain(full + lane, (it - 1) & 1);
-    }
-    return;
-  }
-
-  // ---- consumers -------------------------------------------------------------
   const int g = lane >> 2, t = lane & 3;
-  constexpr int kConsumers = 32 * kWarps;
+
+  const Unpack um = unpack_masks();
+  const float sl2 = a.scale * 1.4426950408889634f, inv_sl2 = 1.f / sl2;
+  Walk w = {};
+  if (works) {
+    w.b = *sm_start;
+    w.v = live_of(a, w.b, fa);
+    const long long at = sm_total[1];
+    w.g = static_cast<int>((R0 - at) / w.v.count);
+    w.row0 = at + static_cast<long long>(w.g) * w.v.count;
+  }
+  // ---- the warp's stream of records -------------------------------------------
+  // Record n of the warp is number warp + kWarps n of the CTA's range and goes
+  // to stage n mod kDepth of the warp's ring.
+  uint8_t* ring = smem + warp * kDepth * L::BYTES;
+  uint64_t* bars = full + warp * kDepth;
+  const long long left = R1 - R0 - warp;
+  const uint32_t total = left > 0 ? static_cast<uint32_t>((left + kWarps - 1) / kWarps) : 0u;
+  uint32_t taken = 0;          // records consumed
+  uint32_t src = kNoRecord;    // lane's record of the current 32 (index into the pool), or none
+  uint32_t missing = 0;        // bit per stage: its record has no valid page
+  bool ok = true;
+  auto fill = [&](uint32_t n) {
+    if ((n & 31u) == 0) {      // places of records n .. n + 31
+      src = kNoRecord;
+      if (n + lane < total) {
+        const long long x = R0 + warp + static_cast<long long>(kWarps) * (n + lane);
+        Walk t = w;
+        while (x >= t.row0 + t.v.count) next_row(a, fa, t);
+        const int k = static_cast<int>(x - t.row0);
+        const int rec = k < t.v.head ? k : t.v.tail + (k - t.v.head);
+        const int recs = a.page_size / kQ4Rec, lp = rec / recs;
+        const int page = a.page_table[static_cast<size_t>(t.b) * a.max_pages + lp];
+        if (page >= 0 && page < a.num_pages)
+          src = (static_cast<uint32_t>(page) * a.Hkv + t.g) * recs + (rec - lp * recs);
+        else
+          raise_error(a.st.err, DEV_ERR_PAGE);
+      }
+      __syncwarp();
+    }
+    const uint32_t idx = __shfl_sync(0xffffffffu, src, n & 31u);
+    const uint32_t stage = n & (kDepth - 1);
+    missing = (missing & ~(1u << stage)) | ((idx == kNoRecord ? 1u : 0u) << stage);
+    if (lane == 0) {
+      if (idx != kNoRecord) {
+        mbar_arrive_expect_tx(bars + stage, L::BYTES);
+        bulk_load(ring + stage * L::BYTES, a.pool + static_cast<size_t>(idx) * L::BYTES, L::BYTES, bars + stage);
+      } else {
+        mbar_arrive(bars + stage);
+      }
+    }
+  };
+  for (uint32_t n = 0; n < kDepth && n < total; ++n) fill(n);
 
   // Sequences with no live token: zero output, lse -inf.
   for (int b = cta; b < a.B; b += gridDim.x) {
@@ -324,23 +336,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
         raise_error(a.st.err, DEV_ERR_SEQLEN);
     }
     uint32_t* o = reinterpret_cast<uint32_t*>(a.o + static_cast<size_t>(b) * a.Hq * D);
-    for (int i = tid; i < a.Hq * (D / 2); i += kConsumers) o[i] = 0;
+    for (int i = tid; i < a.Hq * (D / 2); i += kThreads) o[i] = 0;
     if (a.lse)
-      for (int i = tid; i < a.Hq; i += kConsumers) a.lse[static_cast<size_t>(b) * a.Hq + i] = -INFINITY;
+      for (int i = tid; i < a.Hq; i += kThreads) a.lse[static_cast<size_t>(b) * a.Hq + i] = -INFINITY;
   }
-  if (!works) return;
-
-  const float sl2 = a.scale * 1.4426950408889634f, inv_sl2 = 1.f / sl2;
-  Walk w;
-  w.b = *sm_start;
-  w.v = live_of(a, w.b, fa);
-  {
-    const long long at = sm_total[1];
-    w.g = static_cast<int>((R0 - at) / w.v.count);
-    w.row0 = at + static_cast<long long>(w.g) * w.v.count;
-  }
-  bool ok = true;
-  uint32_t taken = 0;                                            // records this warp has had
   float4* part = reinterpret_cast<float4*>(a.part);              // [2 gridDim][PART4], then m, l [..][8]
   float* part_m = a.part + static_cast<size_t>(2) * gridDim.x * S::PART4 * 4;
   float* part_l = part_m + 2 * gridDim.x * 8;
@@ -382,20 +381,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
     const int skip = (warp + kWarps - static_cast<int>((at - R0) % kWarps)) % kWarps;
     const int k_end = static_cast<int>(end - w.row0);
     for (int k = static_cast<int>(at - w.row0) + skip; k < k_end; k += kWarps, ++taken) {
-      const int stage = warp + kWarps * static_cast<int>(taken & (kDepth - 1));
-      if (ok) ok = mbar_drain(full + stage, (taken / kDepth) & 1, a.st.spin_ns);
-      if (!__all_sync(0xffffffffu, ok)) {
-        if (lane == 0) raise_error(a.st.err, DEV_ERR_TIMEOUT);
-        ok = false;
+      const uint32_t stage = taken & (kDepth - 1), parity = (taken / kDepth) & 1u;
+      if (!ok) continue;
+      if (!__all_sync(0xffffffffu, mbar_try_wait(bars + stage, parity))) {
+        ok = __all_sync(0xffffffffu, mbar_drain(bars + stage, parity, a.st.spin_ns));
+        if (!ok) {             // gave up: the copies in flight land before anything else
+          raise_error(a.st.err, DEV_ERR_TIMEOUT);
+          for (uint32_t n = taken; n < total && n < taken + kDepth; ++n)
+            mbar_drain(bars + (n & (kDepth - 1)), (n / kDepth) & 1u);
+          continue;
+        }
+      }
+      if (missing >> stage & 1u) {
+        if (taken + kDepth < total) fill(taken + kDepth);
         continue;
       }
-      const uint8_t* rec = smem + stage * L::BYTES;
+      const uint8_t* rec = ring + stage * L::BYTES;
       const int u0 = (k < w.v.head ? k : w.v.tail + (k - w.v.head)) * kQ4Rec;
-      if (flag[stage] == 0) {                  // no such page
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty + stage);
-        continue;
-      }
       uint32_t k0[GR], k1[GR], v0[GR], v1[GR];
       float s0[GR], s1[GR];
       load_words<D>(rec + lane * (D / 8), k0);
@@ -408,11 +410,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
       for (int i = 0; i < GR; ++i) {
         float acc[4];
         {
-          const uint32_t af[4] = {k_pair<0>(k0[i]), k_pair<0>(k1[i]), k_pair<1>(k0[i]), k_pair<1>(k1[i])};
+          const uint32_t af[4] = {k_pair<0>(k0[i], um), k_pair<0>(k1[i], um), k_pair<1>(k0[i], um), k_pair<1>(k1[i], um)};
           mma_first(acc, af, qf[i][0], qf[i][1], c0[i], c1[i]);
         }
         {
-          const uint32_t af[4] = {k_pair<2>(k0[i]), k_pair<2>(k1[i]), k_pair<3>(k0[i]), k_pair<3>(k1[i])};
+          const uint32_t af[4] = {k_pair<2>(k0[i], um), k_pair<2>(k1[i], um), k_pair<3>(k0[i], um), k_pair<3>(k1[i], um)};
           mma_bf16_16816(acc, af, qf[i][2], qf[i][3]);
         }
         x00 = fmaf(s0[i], acc[0], x00);
@@ -426,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
       uint32_t sv0 = *reinterpret_cast<const uint32_t*>(vs);
       uint32_t sv1 = *reinterpret_cast<const uint32_t*>(vs + 16);
       __syncwarp();
-      if (lane == 0) mbar_arrive(empty + stage);
+      if (taken + kDepth < total) fill(taken + kDepth);
       // A record at the end of the sequence or of the sink or window: tokens
       // that are not live score -inf, and their values count as zero whatever
       // bytes stand there.
@@ -475,13 +477,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
 #pragma unroll
       for (int j = 0; j < GR; ++j) {
         {
-          const uint32_t af[4] = {fma_bf16x2(v_pair<0>(v0[j]), sv0, n0), fma_bf16x2(v_pair<1>(v0[j]), sv0, n0),
-                                  fma_bf16x2(v_pair<0>(v1[j]), sv1, n1), fma_bf16x2(v_pair<1>(v1[j]), sv1, n1)};
+          const uint32_t af[4] = {fma_bf16x2(v_pair<0>(v0[j], um), sv0, n0), fma_bf16x2(v_pair<1>(v0[j], um), sv0, n0),
+                                  fma_bf16x2(v_pair<0>(v1[j], um), sv1, n1), fma_bf16x2(v_pair<1>(v1[j], um), sv1, n1)};
           mma_bf16_16816(o[2 * j], af, b0, b1);
         }
         {
-          const uint32_t af[4] = {fma_bf16x2(v_pair<2>(v0[j]), sv0, n0), fma_bf16x2(v_pair<3>(v0[j]), sv0, n0),
-                                  fma_bf16x2(v_pair<2>(v1[j]), sv1, n1), fma_bf16x2(v_pair<3>(v1[j]), sv1, n1)};
+          const uint32_t af[4] = {fma_bf16x2(v_pair<2>(v0[j], um), sv0, n0), fma_bf16x2(v_pair<3>(v0[j], um), sv0, n0),
+                                  fma_bf16x2(v_pair<2>(v1[j], um), sv1, n1), fma_bf16x2(v_pair<3>(v1[j], um), sv1, n1)};
           mma_bf16_16816(o[2 * j + 1], af, b0, b1);
         }
       }
@@ -502,10 +504,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
       sm_l[warp * 8 + 2 * t] = l0;
       sm_l[warp * 8 + 2 * t + 1] = l1;
     }
-    const bool fine = named_bar_and(1, kConsumers, ok);
+    const bool fine = named_bar_and(1, kThreads, ok);
     const bool whole = at == w.row0 && end == row1;
     const int slot = 2 * cta + (at == w.row0 ? 1 : 0);
-    for (int i = tid; i < S::PART4; i += kConsumers) {
+    for (int i = tid; i < S::PART4; i += kThreads) {
       const int h = 2 * (i & 3), gi = (i & 31) >> 2, m = i >> 5;
       if (h >= G) continue;
       float M0 = kLowest, M1 = kLowest;
@@ -554,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
       // ---- merge the CTAs of a row: the one that comes last ----------------
       const int first = cta_of(R, N, w.row0), last = cta_of(R, N, row1 - 1);
       __threadfence();
-      named_bar_sync(1, kConsumers);
+      named_bar_sync(1, kThreads);
       if (tid == 0) {
         int* ticket = a.tickets + static_cast<size_t>(w.b) * a.Hkv + w.g;
         const int n = atomicAdd(ticket, 1);
@@ -562,29 +564,29 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
         if (n == last - first) *ticket = 0;
         __threadfence();
       }
-      named_bar_sync(1, kConsumers);
+      named_bar_sync(1, kThreads);
       if (*sm_ticket == last - first) {
         __threadfence();
         // slot of part c: the first CTA's row begins there, the others' before
         const int f0 = 2 * first + 1;
         float* wt = reinterpret_cast<float*>(sm_acc);              // [part][8] weights
         const int np = last - first + 1;
-        for (int i = tid; i < 8 * np; i += kConsumers) {
+        for (int i = tid; i < 8 * np; i += kThreads) {
           const int c = i >> 3, h = i & 7;
           const int sl = c == 0 ? f0 : 2 * (first + c);
           wt[i] = h < G ? __ldcg(part_m + sl * 8 + h) : kLowest;
         }
-        named_bar_sync(1, kConsumers);
+        named_bar_sync(1, kThreads);
         if (tid < 8) {
           float M = kLowest;
           for (int c = 0; c < np; ++c) M = fmaxf(M, wt[c * 8 + tid]);
           sm_fm[tid] = M;
         }
-        named_bar_sync(1, kConsumers);
-        for (int i = tid; i < 8 * np; i += kConsumers) {
+        named_bar_sync(1, kThreads);
+        for (int i = tid; i < 8 * np; i += kThreads) {
           wt[i] = ex2(wt[i] - sm_fm[i & 7]);
         }
-        named_bar_sync(1, kConsumers);
+        named_bar_sync(1, kThreads);
         if (tid < 8 && tid < G) {
           float ls = 0.f;
           bool lost = false;
@@ -598,8 +600,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
           if (a.lse)
             a.lse[head0 + tid] = ls != 0.f ? (sm_fm[tid] + log2f(ls)) * 0.69314718055994531f : -INFINITY;
         }
-        named_bar_sync(1, kConsumers);
-        for (int i = tid; i < S::PART4; i += kConsumers) {
+        named_bar_sync(1, kThreads);
+        for (int i = tid; i < S::PART4; i += kThreads) {
           const int h = 2 * (i & 3), gi = (i & 31) >> 2, m = i >> 5;
           if (h >= G) continue;
           float4 r = {0.f, 0.f, 0.f, 0.f};
@@ -622,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
     at = end;
     if (at < R1) {
       next_row(a, fa, w);
-      named_bar_sync(1, kConsumers);      // the merge buffer is free again
+      named_bar_sync(1, kThreads);      // the merge buffer is free again
     }
   }
 }
