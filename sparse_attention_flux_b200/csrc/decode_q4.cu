@@ -6,27 +6,28 @@
 // is the unpacking, so the kernel is built to keep HBM busy with as few issued
 // instructions per record as possible.
 //
-// Work split.  The live records of all (sequence, kv head) rows are laid end to
+// Work split.  The live records of all (sequence, kv head) rows, in pairs, are laid end to
 // end and cut into equal ranges, one per CTA (two CTAs per SM, one wave), so a
 // ragged batch loads every SM alike.  A CTA walks its range row by row; within
-// a row its warps take records in turn and merge at the row's
+// a row its warps take pairs in turn and merge at the row's
 // end in shared memory.  A row that crosses a range border (at most the first
 // and the last of a CTA) leaves a partial in the workspace; the CTA that
 // delivers a row's last partial (a ticket) merges them in range order, so the
 // result does not depend on timing.
 //
-// Stream.  Each warp keeps a ring of four records in shared memory, filled by
-// bulk copies (a record is one contiguous copy): when the warp has taken a
-// record's operands into registers it refills the stage itself, so a full
-// barrier per stage is all the synchronisation there is.  The places of a
-// warp's next 32 records are looked up at once, a lane each.
+// Stream.  Records are taken in pairs.  Each warp keeps a ring of two pairs in
+// shared memory, filled by bulk copies (one, when the page holds both records):
+// when the warp has taken a pair's operands into registers it refills the stage
+// itself, so a full barrier per stage is all the synchronisation there is.  The
+// places of a warp's next 16 pairs are looked up at once, a lane each record.
 //
 // Arithmetic per record, one warp, warp MMAs (m16n8k16, bf16, fp32 sums):
 //   S = K q^T: the 16 tokens are the rows, the group's query heads (up to 8)
 //     the columns.  A code's 4 bits are a bf16 mantissa's upper bits, so one
 //     AND-OR per pair makes operands 16 + u, u = code + 8; the products of one
-//     32-channel group start from -24 sum(q) and are multiplied by the token's
-//     scale in fp32.
+//     32-channel group are multiplied by the token's scale in fp32.  What the
+//     16 + 8 adds, 24 sum(q) per group, comes off by an MMA of the scales with
+//     it (in three bf16 pieces, 24 bits).
 //   O^T += V^T P^T: the lane's channels are the rows; (16 + u) s - 24 s is one
 //     packed fma and exactly the stored value.  P is rounded to bf16 for the
 //     MMA (the softmax sum keeps fp32 values) and turned by movmatrix.
@@ -41,7 +42,7 @@ namespace {
 
 constexpr int kWarps = 8;                   // per CTA; 16 per SM, 128 registers a thread
 constexpr int kThreads = 32 * kWarps;
-constexpr int kDepth = 4;                   // ring stages of a warp
+constexpr int kDepth = 2;                   // ring stages of a warp, a pair of records each
 constexpr int kStages = kDepth * kWarps;
 constexpr uint32_t kNoRecord = 0xffffffffu;
 constexpr int kCtasPerSm = 2;
@@ -54,7 +55,7 @@ constexpr float kLowest = -3.0e38f;         // reference of a row without tokens
 template <int D>
 struct Q4Smem {
   static constexpr int NT = D / 16;                       // channel tiles
-  static constexpr int RING = kStages * Q4Layout<D>::BYTES;
+  static constexpr int RING = kStages * 2 * Q4Layout<D>::BYTES;
   static constexpr int PART4 = NT * 32;                   // float4 per partial
   static constexpr int ACC = kWarps * PART4 * 16;
   static constexpr int ML = RING + ACC;                   // m, l [warp][8]
@@ -64,10 +65,13 @@ struct Q4Smem {
   static constexpr int BYTES = MISC + 64;
 };
 
-// The live records of one sequence: [0, head) and [tail, end) of its records,
-// `count` of them; the tokens inside them are live below n_sink and from win on.
+// The live records of one sequence: [0, head) and [tail, end) of its records;
+// the tokens inside them are live below n_sink and from win on.  They are taken
+// two at a time: pair j is the live records 2 j and 2 j + 1 (the last may be
+// one).  Pairs below plain1 and from plain2 to plain3 have live tokens only.
 struct Live {
-  int s, n_sink, win, head, tail, count;
+  int s, n_sink, win, head, tail, count, pairs;
+  int plain1, plain2, plain3;
 };
 
 __device__ __forceinline__ Live live_of(const DecodeQ4Launch& a, int b, bool fa) {
@@ -80,37 +84,47 @@ __device__ __forceinline__ Live live_of(const DecodeQ4Launch& a, int b, bool fa)
   v.win = 0;
   v.head = recs;
   v.tail = recs;
+  v.plain2 = v.plain3 = 0;
   if (!fa && s > 0) {
     const int nb = (s - 1) / a.block + 1;
-    v.n_sink = static_cast<int>(min(static_cast<long long>(a.sink_blocks) * a.block,
-                                    static_cast<long long>(s)));
-    v.win = max(0, nb - a.window_blocks) * a.block;
-    v.head = v.n_sink > 0 ? (v.n_sink - 1) / kQ4Rec + 1 : 0;
-    v.tail = max(v.win / kQ4Rec, v.head);
+    const int win = max(0, nb - a.window_blocks) * a.block;
+    const int sink = static_cast<int>(min(static_cast<long long>(a.sink_blocks) * a.block,
+                                          static_cast<long long>(s)));
+    if (win > sink) {
+      v.n_sink = sink;
+      v.win = win;
+      v.head = sink > 0 ? (sink - 1) / kQ4Rec + 1 : 0;
+      v.tail = max(win / kQ4Rec, v.head);
+      const int first = v.tail * kQ4Rec < win ? v.head + 1 : v.head;   // first record behind the border
+      v.plain2 = (first + 1) / 2;
+      v.plain3 = (v.head + s / kQ4Rec - v.tail) / 2;
+    }
   }
+  v.plain1 = v.n_sink / (2 * kQ4Rec);
   v.count = v.head + recs - v.tail;
+  v.pairs = (v.count + 1) / 2;
   return v;
 }
 
 // Walks rows (b, g) in order, skipping sequences without records.
 struct Walk {
   int b, g;
-  long long row0;          // the row's first record in the flat order
+  long long row0;          // the row's first pair in the flat order
   Live v;
 };
 
 __device__ __forceinline__ void next_row(const DecodeQ4Launch& a, bool fa, Walk& w) {
-  w.row0 += w.v.count;
+  w.row0 += w.v.pairs;
   if (++w.g == a.Hkv) {
     w.g = 0;
     do {
       ++w.b;
       if (w.b >= a.B) {    // behind the last row: never reached while records remain
-        w.v.count = 0x7fffffff;
+        w.v.pairs = 0x7fffffff;
         return;
       }
       w.v = live_of(a, w.b, fa);
-    } while (w.v.count == 0);
+    } while (w.v.pairs == 0);
   }
 }
 
@@ -134,14 +148,13 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t x, uint32_t y, uint32_t 
   return r;
 }
 
-// d = a b + c with c held elsewhere.
-__device__ __forceinline__ void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                          uint32_t b1, float c0, float c1) {
+// d = a b.
+__device__ __forceinline__ void mma_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%10,%11,%10,%11};"
+      "{%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // (x & code) | base with both constants in registers: one LOP3.
@@ -200,7 +213,7 @@ __device__ __forceinline__ void load_scales(const uint8_t* p, float (&s)[D / 32]
   }
 }
 
-// First record of CTA c's range, and the CTA of a record, for R records in N ranges.
+// First pair of CTA c's range, and the CTA of a pair, for R pairs in N ranges.
 __device__ __forceinline__ long long range_of(long long R, int N, int c) { return R * c / N; }
 __device__ __forceinline__ int cta_of(long long R, int N, long long x) {
   return static_cast<int>(((x + 1) * N - 1) / R);
@@ -231,12 +244,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
   const bool fa = a.layer_mode == nullptr || a.layer_mode[a.layer] != 0;
   const int G = a.Hq / a.Hkv;
 
-  // ---- records of all rows, and where this CTA's range starts -------------
-  // Thread t owns `per` consecutive sequences; a block scan of their records.
+  // ---- pairs of all rows, and where this CTA's range starts -------------
+  // Thread t owns `per` consecutive sequences; a block scan of their pairs.
   const int per = (a.B + kThreads - 1) / kThreads;
   const int bt0 = tid * per, bt1 = min(bt0 + per, a.B);
   long long mine = 0;
-  for (int b = bt0; b < bt1; ++b) mine += live_of(a, b, fa).count;
+  for (int b = bt0; b < bt1; ++b) mine += live_of(a, b, fa).pairs;
   mine *= a.Hkv;
   long long incl = mine;
 #pragma unroll
@@ -254,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
     if (w < warp) before += x;
     R += x;
   }
-  // At least one record per warp before another CTA joins in.
+  // At least one pair per warp before another CTA joins in.
   const int N = static_cast<int>(min(static_cast<long long>(gridDim.x), (R + kWarps - 1) / kWarps));
   const int cta = blockIdx.x;
   const bool works = cta < N;
@@ -263,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
     long long at = before;
     int b = bt0;
     for (;; ++b) {
-      const long long n = static_cast<long long>(live_of(a, b, fa).count) * a.Hkv;
+      const long long n = static_cast<long long>(live_of(a, b, fa).pairs) * a.Hkv;
       if (R0 < at + n) break;
       at += n;
     }
@@ -281,47 +294,63 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
     w.b = *sm_start;
     w.v = live_of(a, w.b, fa);
     const long long at = sm_total[1];
-    w.g = static_cast<int>((R0 - at) / w.v.count);
-    w.row0 = at + static_cast<long long>(w.g) * w.v.count;
+    w.g = static_cast<int>((R0 - at) / w.v.pairs);
+    w.row0 = at + static_cast<long long>(w.g) * w.v.pairs;
   }
-  // ---- the warp's stream of records -------------------------------------------
-  // Record n of the warp is number warp + kWarps n of the CTA's range and goes
+  // ---- the warp's stream of pairs ---------------------------------------------
+  // Pair n of the warp is number warp + kWarps n of the CTA's range and goes
   // to stage n mod kDepth of the warp's ring.
-  uint8_t* ring = smem + warp * kDepth * L::BYTES;
+  uint8_t* ring = smem + warp * kDepth * 2 * L::BYTES;
   uint64_t* bars = full + warp * kDepth;
   const long long left = R1 - R0 - warp;
   const uint32_t total = left > 0 ? static_cast<uint32_t>((left + kWarps - 1) / kWarps) : 0u;
-  uint32_t taken = 0;          // records consumed
-  uint32_t src = kNoRecord;    // lane's record of the current 32 (index into the pool), or none
-  uint32_t missing = 0;        // bit per stage: its record has no valid page
+  uint32_t taken = 0;          // pairs consumed
+  uint32_t src = kNoRecord;    // lane's record of the current 16 pairs (index into the pool), or none
+  uint32_t missing = 0;        // two bits per stage: no such record
   bool ok = true;
   auto fill = [&](uint32_t n) {
-    if ((n & 31u) == 0) {      // places of records n .. n + 31
+    if ((n & 15u) == 0) {      // places of pairs n .. n + 15
       src = kNoRecord;
-      if (n + lane < total) {
-        const long long x = R0 + warp + static_cast<long long>(kWarps) * (n + lane);
+      const uint32_t nl = n + (lane >> 1);
+      if (nl < total) {
+        const long long x = R0 + warp + static_cast<long long>(kWarps) * nl;
         Walk t = w;
-        while (x >= t.row0 + t.v.count) next_row(a, fa, t);
-        const int k = static_cast<int>(x - t.row0);
-        const int rec = k < t.v.head ? k : t.v.tail + (k - t.v.head);
-        const int recs = a.page_size / kQ4Rec, lp = rec / recs;
-        const int page = a.page_table[static_cast<size_t>(t.b) * a.max_pages + lp];
-        if (page >= 0 && page < a.num_pages)
-          src = (static_cast<uint32_t>(page) * a.Hkv + t.g) * recs + (rec - lp * recs);
-        else
-          raise_error(a.st.err, DEV_ERR_PAGE);
+        while (x >= t.row0 + t.v.pairs) next_row(a, fa, t);
+        const int k = 2 * static_cast<int>(x - t.row0) + (lane & 1);
+        if (k < t.v.count) {
+          const int rec = k < t.v.head ? k : t.v.tail + (k - t.v.head);
+          const int recs = a.page_size / kQ4Rec, lp = rec / recs;
+          const int page = a.page_table[static_cast<size_t>(t.b) * a.max_pages + lp];
+          if (page >= 0 && page < a.num_pages)
+            src = (static_cast<uint32_t>(page) * a.Hkv + t.g) * recs + (rec - lp * recs);
+          else
+            raise_error(a.st.err, DEV_ERR_PAGE);
+        }
       }
       __syncwarp();
     }
-    const uint32_t idx = __shfl_sync(0xffffffffu, src, n & 31u);
+    const uint32_t i0 = __shfl_sync(0xffffffffu, src, (2 * n) & 31u);
+    const uint32_t i1 = __shfl_sync(0xffffffffu, src, (2 * n + 1) & 31u);
     const uint32_t stage = n & (kDepth - 1);
-    missing = (missing & ~(1u << stage)) | ((idx == kNoRecord ? 1u : 0u) << stage);
+    const uint32_t none = (i0 == kNoRecord ? 1u : 0u) | (i1 == kNoRecord ? 2u : 0u);
+    missing = (missing & ~(3u << (2 * stage))) | (none << (2 * stage));
     if (lane == 0) {
-      if (idx != kNoRecord) {
-        mbar_arrive_expect_tx(bars + stage, L::BYTES);
-        bulk_load(ring + stage * L::BYTES, a.pool + static_cast<size_t>(idx) * L::BYTES, L::BYTES, bars + stage);
-      } else {
+      uint8_t* dst = ring + stage * 2 * L::BYTES;
+      const uint8_t* from = a.pool + static_cast<size_t>(i0) * L::BYTES;
+      if (none == 0) {
+        mbar_arrive_expect_tx(bars + stage, 2 * L::BYTES);
+        if (i1 == i0 + 1) {
+          bulk_load(dst, from, 2 * L::BYTES, bars + stage);
+        } else {
+          bulk_load(dst, from, L::BYTES, bars + stage);
+          bulk_load(dst + L::BYTES, a.pool + static_cast<size_t>(i1) * L::BYTES, L::BYTES, bars + stage);
+        }
+      } else if (none == 3) {
         mbar_arrive(bars + stage);
+      } else {
+        mbar_arrive_expect_tx(bars + stage, L::BYTES);
+        if (none == 2) bulk_load(dst, from, L::BYTES, bars + stage);
+        else bulk_load(dst + L::BYTES, a.pool + static_cast<size_t>(i1) * L::BYTES, L::BYTES, bars + stage);
       }
     }
   };
@@ -329,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
 
   // Sequences with no live token: zero output, lse -inf.
   for (int b = cta; b < a.B; b += gridDim.x) {
-    if (live_of(a, b, fa).count != 0) continue;
+    if (live_of(a, b, fa).pairs != 0) continue;
     if (tid == 0) {
       const int s = a.seqlens[b];
       if (s < 0 || s > static_cast<long long>(a.max_pages) * a.page_size)
@@ -345,29 +374,53 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
   float* part_l = part_m + 2 * gridDim.x * 8;
 
   for (long long at = R0; at < R1;) {
-    const long long row1 = w.row0 + w.v.count;
+    const long long row1 = w.row0 + w.v.pairs;
     const long long end = min(row1, R1);
     const size_t head0 = static_cast<size_t>(w.b) * a.Hq + w.g * G;   // the group's first query head
 
-    // Query operands: lane 4 g + t holds head g, channels 32 w + 8 t + e; and
-    // -24 times the group sums of heads 2 t and 2 t + 1.
-    uint32_t qf[GR][4];
-    float c0[GR], c1[GR];
+    // Query operands: lane 4 g + t holds head g, channels 32 i + 8 t + e.  And
+    // -24 times the head's group sums, cut into three bf16 numbers, as the
+    // second operand of an MMA whose first is the tokens' scales: row 2 t + e
+    // of that product is (at d 128) piece t / 2 of group 2 (t % 2) + e, rows 8
+    // and up the last piece; at d 64 piece t of group e.
+    uint32_t qf[GR][4], bq0 = 0, bq1 = 0;
+    {
+      float c[GR];
 #pragma unroll
-    for (int i = 0; i < GR; ++i) {
-      uint4 v = {0, 0, 0, 0};
-      if (g < G) v = *reinterpret_cast<const uint4*>(a.q + (head0 + g) * D + 32 * i + 8 * t);
-      qf[i][0] = v.x;
-      qf[i][1] = v.y;
-      qf[i][2] = v.z;
-      qf[i][3] = v.w;
-      float sum = 0.f;
+      for (int i = 0; i < GR; ++i) {
+        uint4 v = {0, 0, 0, 0};
+        if (g < G) v = *reinterpret_cast<const uint4*>(a.q + (head0 + g) * D + 32 * i + 8 * t);
+        qf[i][0] = v.x;
+        qf[i][1] = v.y;
+        qf[i][2] = v.z;
+        qf[i][3] = v.w;
+        float sum = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sum += bf16lo_to_f32(qf[i][e]) + bf16hi_to_f32(qf[i][e]);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      c0[i] = -24.f * __shfl_sync(0xffffffffu, sum, 8 * t);
-      c1[i] = -24.f * __shfl_sync(0xffffffffu, sum, 8 * t + 4);
+        for (int e = 0; e < 4; ++e) sum += bf16lo_to_f32(qf[i][e]) + bf16hi_to_f32(qf[i][e]);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        c[i] = -24.f * sum;
+      }
+      float e0 = c[0], e1 = c[1];
+      if constexpr (D == 128) {
+        if (t & 1) {
+          e0 = c[2];
+          e1 = c[3];
+        }
+      }
+      const uint32_t hi = pack_bf16x2(e0, e1);
+      e0 -= bf16lo_to_f32(hi);
+      e1 -= bf16hi_to_f32(hi);
+      const uint32_t mid = pack_bf16x2(e0, e1);
+      e0 -= bf16lo_to_f32(mid);
+      e1 -= bf16hi_to_f32(mid);
+      const uint32_t lo = pack_bf16x2(e0, e1);
+      if constexpr (D == 128) {
+        bq0 = t < 2 ? hi : mid;
+        bq1 = t < 2 ? lo : 0u;
+      } else {
+        bq0 = t == 0 ? hi : t == 1 ? mid : t == 2 ? lo : 0u;
+      }
     }
 
     float o[NT][4];
@@ -377,10 +430,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
     float m0 = kLowest, m1 = kLowest;          // softmax references (log2 units) of heads 2 t, 2 t + 1
     float th0 = kLowest, th1 = kLowest;        // a score (before the scale) above it moves the reference
 
-    // The warp takes every kWarps-th record of the CTA's range.
+    // The warp takes every kWarps-th pair of the CTA's range.
     const int skip = (warp + kWarps - static_cast<int>((at - R0) % kWarps)) % kWarps;
-    const int k_end = static_cast<int>(end - w.row0);
-    for (int k = static_cast<int>(at - w.row0) + skip; k < k_end; k += kWarps, ++taken) {
+    const int j_end = static_cast<int>(end - w.row0);
+    for (int j = static_cast<int>(at - w.row0) + skip; j < j_end; j += kWarps, ++taken) {
       const uint32_t stage = taken & (kDepth - 1), parity = (taken / kDepth) & 1u;
       if (!ok) continue;
       if (!__all_sync(0xffffffffu, mbar_try_wait(bars + stage, parity))) {
@@ -392,56 +445,77 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
           continue;
         }
       }
-      if (missing >> stage & 1u) {
-        if (taken + kDepth < total) fill(taken + kDepth);
-        continue;
-      }
-      const uint8_t* rec = ring + stage * L::BYTES;
-      const int u0 = (k < w.v.head ? k : w.v.tail + (k - w.v.head)) * kQ4Rec;
-      uint32_t k0[GR], k1[GR], v0[GR], v1[GR];
-      float s0[GR], s1[GR];
-      load_words<D>(rec + lane * (D / 8), k0);
-      load_words<D>(rec + 4 * D + lane * (D / 8), k1);
-      load_scales<D>(rec + L::KS + g * (2 * GR), s0);
-      load_scales<D>(rec + L::KS + (g + 8) * (2 * GR), s1);
+      const uint32_t none = missing >> (2 * stage) & 3u;
+      const uint8_t* rec = ring + stage * 2 * L::BYTES;
 
-      float x00 = 0.f, x01 = 0.f, x10 = 0.f, x11 = 0.f;
+      float x[2][4];           // scores: tokens g, g + 8, heads 2 t, 2 t + 1
 #pragma unroll
-      for (int i = 0; i < GR; ++i) {
-        float acc[4];
+      for (int r = 0; r < 2; ++r) {
+        const uint8_t* p = rec + r * L::BYTES;
+        uint32_t k0[GR], k1[GR];
+        float s0[GR], s1[GR];
+        load_words<D>(p + lane * (D / 8), k0);
+        load_words<D>(p + 4 * D + lane * (D / 8), k1);
+        load_scales<D>(p + L::KS + g * (2 * GR), s0);
+        load_scales<D>(p + L::KS + (g + 8) * (2 * GR), s1);
         {
-          const uint32_t af[4] = {k_pair<0>(k0[i], um), k_pair<0>(k1[i], um), k_pair<1>(k0[i], um), k_pair<1>(k1[i], um)};
-          mma_first(acc, af, qf[i][0], qf[i][1], c0[i], c1[i]);
+          const uint32_t w0 = *reinterpret_cast<const uint32_t*>(p + L::KS + g * (2 * GR) + (t & (GR / 2 - 1)) * 4);
+          const uint32_t w1 =
+              *reinterpret_cast<const uint32_t*>(p + L::KS + (g + 8) * (2 * GR) + (t & (GR / 2 - 1)) * 4);
+          const uint32_t af[4] = {w0, w1, w0, w1};
+          mma_zero(x[r], af, bq0, bq1);
         }
-        {
-          const uint32_t af[4] = {k_pair<2>(k0[i], um), k_pair<2>(k1[i], um), k_pair<3>(k0[i], um), k_pair<3>(k1[i], um)};
-          mma_bf16_16816(acc, af, qf[i][2], qf[i][3]);
+#pragma unroll
+        for (int i = 0; i < GR; ++i) {
+          float acc[4];
+          {
+            const uint32_t af[4] = {k_pair<0>(k0[i], um), k_pair<0>(k1[i], um), k_pair<1>(k0[i], um),
+                                    k_pair<1>(k1[i], um)};
+            mma_zero(acc, af, qf[i][0], qf[i][1]);
+          }
+          {
+            const uint32_t af[4] = {k_pair<2>(k0[i], um), k_pair<2>(k1[i], um), k_pair<3>(k0[i], um),
+                                    k_pair<3>(k1[i], um)};
+            mma_bf16_16816(acc, af, qf[i][2], qf[i][3]);
+          }
+          x[r][0] = fmaf(s0[i], acc[0], x[r][0]);
+          x[r][1] = fmaf(s0[i], acc[1], x[r][1]);
+          x[r][2] = fmaf(s1[i], acc[2], x[r][2]);
+          x[r][3] = fmaf(s1[i], acc[3], x[r][3]);
         }
-        x00 = fmaf(s0[i], acc[0], x00);
-        x01 = fmaf(s0[i], acc[1], x01);
-        x10 = fmaf(s1[i], acc[2], x10);
-        x11 = fmaf(s1[i], acc[3], x11);
       }
-      load_words<D>(rec + L::VC + lane * (D / 8), v0);
-      load_words<D>(rec + L::VC + 4 * D + lane * (D / 8), v1);
-      const uint8_t* vs = rec + L::VS + (g * (D / 8) / 32) * 32 + 4 * t;
-      uint32_t sv0 = *reinterpret_cast<const uint32_t*>(vs);
-      uint32_t sv1 = *reinterpret_cast<const uint32_t*>(vs + 16);
+      uint32_t v0[2][GR], v1[2][GR], sv0[2], sv1[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint8_t* p = rec + r * L::BYTES;
+        load_words<D>(p + L::VC + lane * (D / 8), v0[r]);
+        load_words<D>(p + L::VC + 4 * D + lane * (D / 8), v1[r]);
+        const uint8_t* vs = p + L::VS + (g * (D / 8) / 32) * 32 + 4 * t;
+        sv0[r] = *reinterpret_cast<const uint32_t*>(vs);
+        sv1[r] = *reinterpret_cast<const uint32_t*>(vs + 16);
+      }
       __syncwarp();
       if (taken + kDepth < total) fill(taken + kDepth);
-      // A record at the end of the sequence or of the sink or window: tokens
-      // that are not live score -inf, and their values count as zero whatever
-      // bytes stand there.
-      if (!(w.v.s - u0 >= kQ4Rec && (w.v.n_sink - u0 >= kQ4Rec || u0 >= w.v.win))) {
-        auto live = [&](int u) { return u < w.v.s && (u < w.v.n_sink || u >= w.v.win); };
-        if (!live(u0 + g)) x00 = x01 = -INFINITY;
-        if (!live(u0 + g + 8)) x10 = x11 = -INFINITY;
-        if (!live(u0 + 2 * t)) sv0 &= 0xffff0000u;
-        if (!live(u0 + 2 * t + 1)) sv0 &= 0x0000ffffu;
-        if (!live(u0 + 2 * t + 8)) sv1 &= 0xffff0000u;
-        if (!live(u0 + 2 * t + 9)) sv1 &= 0x0000ffffu;
+      // A pair at the end of the sequence or of the sink or window, or with a
+      // missing page: tokens that are not live score -inf, and their values
+      // count as zero whatever bytes stand there.
+      if (none != 0 || !(j < w.v.plain1 || (j >= w.v.plain2 && j < w.v.plain3))) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int k = 2 * j + r;
+          const int u0 = (k < w.v.head ? k : w.v.tail + (k - w.v.head)) * kQ4Rec;
+          const bool there = !(none >> r & 1u);
+          auto live = [&](int u) { return there && u < w.v.s && (u < w.v.n_sink || u >= w.v.win); };
+          if (!live(u0 + g)) x[r][0] = x[r][1] = -INFINITY;
+          if (!live(u0 + g + 8)) x[r][2] = x[r][3] = -INFINITY;
+          if (!live(u0 + 2 * t)) sv0[r] &= 0xffff0000u;
+          if (!live(u0 + 2 * t + 1)) sv0[r] &= 0x0000ffffu;
+          if (!live(u0 + 2 * t + 8)) sv1[r] &= 0xffff0000u;
+          if (!live(u0 + 2 * t + 9)) sv1[r] &= 0x0000ffffu;
+        }
       }
-      const float t0 = fmaxf(x00, x10), t1 = fmaxf(x01, x11);
+      const float t0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
+      const float t1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
       if (__any_sync(0xffffffffu, t0 > th0 || t1 > th1)) {
         float n0 = t0, n1 = t1;
 #pragma unroll
@@ -466,25 +540,31 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
           o[m][3] *= f1;
         }
       }
-      const float p00 = ex2(fmaf(x00, sl2, -m0)), p01 = ex2(fmaf(x01, sl2, -m1));
-      const float p10 = ex2(fmaf(x10, sl2, -m0)), p11 = ex2(fmaf(x11, sl2, -m1));
-      l0 += p00 + p10;
-      l1 += p01 + p11;
-      const uint32_t b0 = movmatrix_trans(pack_bf16x2(p00, p01));
-      const uint32_t b1 = movmatrix_trans(pack_bf16x2(p10, p11));
-      // -24 s (exact: 5 bits times 3)
-      const uint32_t n0 = fma_bf16x2(sv0, 0xc1c0c1c0u, 0u), n1 = fma_bf16x2(sv1, 0xc1c0c1c0u, 0u);
 #pragma unroll
-      for (int j = 0; j < GR; ++j) {
-        {
-          const uint32_t af[4] = {fma_bf16x2(v_pair<0>(v0[j], um), sv0, n0), fma_bf16x2(v_pair<1>(v0[j], um), sv0, n0),
-                                  fma_bf16x2(v_pair<0>(v1[j], um), sv1, n1), fma_bf16x2(v_pair<1>(v1[j], um), sv1, n1)};
-          mma_bf16_16816(o[2 * j], af, b0, b1);
-        }
-        {
-          const uint32_t af[4] = {fma_bf16x2(v_pair<2>(v0[j], um), sv0, n0), fma_bf16x2(v_pair<3>(v0[j], um), sv0, n0),
-                                  fma_bf16x2(v_pair<2>(v1[j], um), sv1, n1), fma_bf16x2(v_pair<3>(v1[j], um), sv1, n1)};
-          mma_bf16_16816(o[2 * j + 1], af, b0, b1);
+      for (int r = 0; r < 2; ++r) {
+        const float p00 = ex2(fmaf(x[r][0], sl2, -m0)), p01 = ex2(fmaf(x[r][1], sl2, -m1));
+        const float p10 = ex2(fmaf(x[r][2], sl2, -m0)), p11 = ex2(fmaf(x[r][3], sl2, -m1));
+        l0 += p00 + p10;
+        l1 += p01 + p11;
+        const uint32_t b0 = movmatrix_trans(pack_bf16x2(p00, p01));
+        const uint32_t b1 = movmatrix_trans(pack_bf16x2(p10, p11));
+        // -24 s (exact: 5 bits times 3)
+        const uint32_t n0 = fma_bf16x2(sv0[r], 0xc1c0c1c0u, 0u), n1 = fma_bf16x2(sv1[r], 0xc1c0c1c0u, 0u);
+#pragma unroll
+        for (int i = 0; i < GR; ++i) {
+          const uint32_t a0 = v0[r][i], a1 = v1[r][i];
+          {
+            const uint32_t af[4] = {
+                fma_bf16x2(v_pair<0>(a0, um), sv0[r], n0), fma_bf16x2(v_pair<1>(a0, um), sv0[r], n0),
+                fma_bf16x2(v_pair<0>(a1, um), sv1[r], n1), fma_bf16x2(v_pair<1>(a1, um), sv1[r], n1)};
+            mma_bf16_16816(o[2 * i], af, b0, b1);
+          }
+          {
+            const uint32_t af[4] = {
+                fma_bf16x2(v_pair<2>(a0, um), sv0[r], n0), fma_bf16x2(v_pair<3>(a0, um), sv0[r], n0),
+                fma_bf16x2(v_pair<2>(a1, um), sv1[r], n1), fma_bf16x2(v_pair<3>(a1, um), sv1[r], n1)};
+            mma_bf16_16816(o[2 * i + 1], af, b0, b1);
+          }
         }
       }
     }
