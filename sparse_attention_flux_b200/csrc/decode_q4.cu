@@ -8,7 +8,9 @@
 //
 // Work split.  The live records of all (sequence, kv head) rows, in pairs, are laid end to
 // end and cut into equal ranges, one per CTA (two CTAs per SM, one wave), so a
-// ragged batch loads every SM alike.  A CTA walks its range row by row; within
+// ragged batch loads every SM alike; a row counts kRowCost empty slots more
+// than its pairs, since its merge takes about as long (without them the CTA
+// that gets a batch's short requests, 45 rows, took 90 us of a 30 us call).  A CTA walks its range row by row; within
 // a row its warps take pairs in turn and merge at the row's
 // end in shared memory.  A row that crosses a range border (at most the first
 // and the last of a CTA) leaves a partial in the workspace; the CTA that
@@ -44,6 +46,7 @@ constexpr int kWarps = 8;                   // per CTA; 16 per SM, 128 registers
 constexpr int kThreads = 32 * kWarps;
 constexpr int kDepth = 2;                   // ring stages of a warp, a pair of records each
 constexpr int kStages = kDepth * kWarps;
+constexpr int kRowCost = kWarps;            // what a row's merge costs, in pairs of the split (below)
 constexpr uint32_t kNoRecord = 0xffffffffu;
 constexpr int kCtasPerSm = 2;
 constexpr float kGrow = 8.f;                // log2 growth of a score that is tolerated
@@ -70,7 +73,7 @@ struct Q4Smem {
 // two at a time: pair j is the live records 2 j and 2 j + 1 (the last may be
 // one).  Pairs below plain1 and from plain2 to plain3 have live tokens only.
 struct Live {
-  int s, n_sink, win, head, tail, count, pairs;
+  int s, n_sink, win, head, tail, count, pairs, slots;
   int plain1, plain2, plain3;
 };
 
@@ -103,28 +106,29 @@ __device__ __forceinline__ Live live_of(const DecodeQ4Launch& a, int b, bool fa)
   v.plain1 = v.n_sink / (2 * kQ4Rec);
   v.count = v.head + recs - v.tail;
   v.pairs = (v.count + 1) / 2;
+  v.slots = v.pairs > 0 ? v.pairs + kRowCost : 0;
   return v;
 }
 
 // Walks rows (b, g) in order, skipping sequences without records.
 struct Walk {
   int b, g;
-  long long row0;          // the row's first pair in the flat order
+  long long row0;          // the row's first slot in the flat order
   Live v;
 };
 
 __device__ __forceinline__ void next_row(const DecodeQ4Launch& a, bool fa, Walk& w) {
-  w.row0 += w.v.pairs;
+  w.row0 += w.v.slots;
   if (++w.g == a.Hkv) {
     w.g = 0;
     do {
       ++w.b;
       if (w.b >= a.B) {    // behind the last row: never reached while records remain
-        w.v.pairs = 0x7fffffff;
+        w.v.slots = 0x7fffffff;
         return;
       }
       w.v = live_of(a, w.b, fa);
-    } while (w.v.pairs == 0);
+    } while (w.v.slots == 0);
   }
 }
 
@@ -213,7 +217,7 @@ __device__ __forceinline__ void load_scales(const uint8_t* p, float (&s)[D / 32]
   }
 }
 
-// First pair of CTA c's range, and the CTA of a pair, for R pairs in N ranges.
+// First slot of CTA c's range, and the CTA of a slot, for R slots in N ranges.
 __device__ __forceinline__ long long range_of(long long R, int N, int c) { return R * c / N; }
 __device__ __forceinline__ int cta_of(long long R, int N, long long x) {
   return static_cast<int>(((x + 1) * N - 1) / R);
@@ -244,12 +248,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
   const bool fa = a.layer_mode == nullptr || a.layer_mode[a.layer] != 0;
   const int G = a.Hq / a.Hkv;
 
-  // ---- pairs of all rows, and where this CTA's range starts -------------
-  // Thread t owns `per` consecutive sequences; a block scan of their pairs.
+  // ---- slots of all rows, and where this CTA's range starts -------------
+  // Thread t owns `per` consecutive sequences; a block scan of their slots.
   const int per = (a.B + kThreads - 1) / kThreads;
   const int bt0 = tid * per, bt1 = min(bt0 + per, a.B);
   long long mine = 0;
-  for (int b = bt0; b < bt1; ++b) mine += live_of(a, b, fa).pairs;
+  for (int b = bt0; b < bt1; ++b) mine += live_of(a, b, fa).slots;
   mine *= a.Hkv;
   long long incl = mine;
 #pragma unroll
@@ -267,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
     if (w < warp) before += x;
     R += x;
   }
-  // At least one pair per warp before another CTA joins in.
+  // At least one slot per warp before another CTA joins in.
   const int N = static_cast<int>(min(static_cast<long long>(gridDim.x), (R + kWarps - 1) / kWarps));
   const int cta = blockIdx.x;
   const bool works = cta < N;
@@ -276,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
     long long at = before;
     int b = bt0;
     for (;; ++b) {
-      const long long n = static_cast<long long>(live_of(a, b, fa).pairs) * a.Hkv;
+      const long long n = static_cast<long long>(live_of(a, b, fa).slots) * a.Hkv;
       if (R0 < at + n) break;
       at += n;
     }
@@ -294,17 +298,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
     w.b = *sm_start;
     w.v = live_of(a, w.b, fa);
     const long long at = sm_total[1];
-    w.g = static_cast<int>((R0 - at) / w.v.pairs);
-    w.row0 = at + static_cast<long long>(w.g) * w.v.pairs;
+    w.g = static_cast<int>((R0 - at) / w.v.slots);
+    w.row0 = at + static_cast<long long>(w.g) * w.v.slots;
   }
-  // ---- the warp's stream of pairs ---------------------------------------------
-  // Pair n of the warp is number warp + kWarps n of the CTA's range and goes
+  // ---- the warp's stream of slots ---------------------------------------------
+  // Slot n of the warp is number warp + kWarps n of the CTA's range and goes
   // to stage n mod kDepth of the warp's ring.
   uint8_t* ring = smem + warp * kDepth * 2 * L::BYTES;
   uint64_t* bars = full + warp * kDepth;
   const long long left = R1 - R0 - warp;
   const uint32_t total = left > 0 ? static_cast<uint32_t>((left + kWarps - 1) / kWarps) : 0u;
-  uint32_t taken = 0;          // pairs consumed
+  uint32_t taken = 0;          // slots consumed
   uint32_t src = kNoRecord;    // lane's record of the current 16 pairs (index into the pool), or none
   uint32_t missing = 0;        // two bits per stage: no such record
   bool ok = true;
@@ -315,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
       if (nl < total) {
         const long long x = R0 + warp + static_cast<long long>(kWarps) * nl;
         Walk t = w;
-        while (x >= t.row0 + t.v.pairs) next_row(a, fa, t);
+        while (x >= t.row0 + t.v.slots) next_row(a, fa, t);
         const int k = 2 * static_cast<int>(x - t.row0) + (lane & 1);
         if (k < t.v.count) {
           const int rec = k < t.v.head ? k : t.v.tail + (k - t.v.head);
@@ -375,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
 
   for (long long at = R0; at < R1;) {
     const long long row1 = w.row0 + w.v.pairs;
-    const long long end = min(row1, R1);
+    const long long end = min(w.row0 + w.v.slots, R1);
     const size_t head0 = static_cast<size_t>(w.b) * a.Hq + w.g * G;   // the group's first query head
 
     // Query operands: lane 4 g + t holds head g, channels 32 i + 8 t + e.  And
@@ -423,6 +427,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
       }
     }
 
+    // The next row's query, for when it is its turn.
+    if (end < R1 && lane < G * D / 64 && head0 + 2 * G <= static_cast<size_t>(a.B) * a.Hq)
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(a.q + (head0 + G) * D + lane * 64));
+
     float o[NT][4];
 #pragma unroll
     for (int m = 0; m < NT; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
@@ -430,12 +438,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
     float m0 = kLowest, m1 = kLowest;          // softmax references (log2 units) of heads 2 t, 2 t + 1
     float th0 = kLowest, th1 = kLowest;        // a score (before the scale) above it moves the reference
 
-    // The warp takes every kWarps-th pair of the CTA's range.
+    // The warp takes every kWarps-th slot of the CTA's range.
     const int skip = (warp + kWarps - static_cast<int>((at - R0) % kWarps)) % kWarps;
     const int j_end = static_cast<int>(end - w.row0);
     for (int j = static_cast<int>(at - w.row0) + skip; j < j_end; j += kWarps, ++taken) {
       const uint32_t stage = taken & (kDepth - 1), parity = (taken / kDepth) & 1u;
+      const uint32_t none = missing >> (2 * stage) & 3u;
       if (!ok) continue;
+      if (none == 3u) {        // an empty slot, or no valid page: nothing was copied
+        if (taken + kDepth < total) fill(taken + kDepth);
+        continue;
+      }
       if (!__all_sync(0xffffffffu, mbar_try_wait(bars + stage, parity))) {
         ok = __all_sync(0xffffffffu, mbar_drain(bars + stage, parity, a.st.spin_ns));
         if (!ok) {             // gave up: the copies in flight land before anything else
@@ -445,7 +458,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
           continue;
         }
       }
-      const uint32_t none = missing >> (2 * stage) & 3u;
       const uint8_t* rec = ring + stage * 2 * L::BYTES;
 
       float x[2][4];           // scores: tokens g, g + 8, heads 2 t, 2 t + 1
@@ -569,6 +581,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
       }
     }
 
+    if (at >= row1) {          // the range begins in the row's empty slots
+      at = end;
+      if (at < R1) next_row(a, fa, w);
+      continue;
+    }
     // ---- merge the warps --------------------------------------------------
 #pragma unroll
     for (int s = 4; s < 32; s <<= 1) {
@@ -585,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
       sm_l[warp * 8 + 2 * t + 1] = l1;
     }
     const bool fine = named_bar_and(1, kThreads, ok);
-    const bool whole = at == w.row0 && end == row1;
+    const bool whole = at == w.row0 && end >= row1;
     const int slot = 2 * cta + (at == w.row0 ? 1 : 0);
     for (int i = tid; i < S::PART4; i += kThreads) {
       const int h = 2 * (i & 3), gi = (i & 31) >> 2, m = i >> 5;
