@@ -73,7 +73,7 @@ struct Q4Smem {
 // two at a time: pair j is the live records 2 j and 2 j + 1 (the last may be
 // one).  Pairs below plain1 and from plain2 to plain3 have live tokens only.
 struct Live {
-  int s, n_sink, win, head, tail, count, pairs, slots;
+  int s, n_sink, win, head, tail, count, pairs;
   int plain1, plain2, plain3;
 };
 
@@ -106,29 +106,28 @@ __device__ __forceinline__ Live live_of(const DecodeQ4Launch& a, int b, bool fa)
   v.plain1 = v.n_sink / (2 * kQ4Rec);
   v.count = v.head + recs - v.tail;
   v.pairs = (v.count + 1) / 2;
-  v.slots = v.pairs > 0 ? v.pairs + kRowCost : 0;
   return v;
 }
 
-// Walks rows (b, g) in order, skipping sequences without records.
-struct Walk {
+__device__ __forceinline__ int slots_of(const Live& v) { return v.pairs > 0 ? v.pairs + kRowCost : 0; }
+
+// Row (b, g) and its slots; rows without records are skipped.
+struct Row {
   int b, g;
-  long long row0;          // the row's first slot in the flat order
-  Live v;
+  uint32_t slots;
 };
 
-__device__ __forceinline__ void next_row(const DecodeQ4Launch& a, bool fa, Walk& w) {
-  w.row0 += w.v.slots;
+__device__ __forceinline__ void next_row(const DecodeQ4Launch& a, bool fa, Row& w) {
   if (++w.g == a.Hkv) {
     w.g = 0;
     do {
       ++w.b;
       if (w.b >= a.B) {    // behind the last row: never reached while records remain
-        w.v.slots = 0x7fffffff;
+        w.slots = 0xffffffffu;
         return;
       }
-      w.v = live_of(a, w.b, fa);
-    } while (w.v.slots == 0);
+      w.slots = slots_of(live_of(a, w.b, fa));
+    } while (w.slots == 0);
   }
 }
 
@@ -142,7 +141,7 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 
@@ -152,9 +151,16 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t x, uint32_t y, uint32_t 
   return r;
 }
 
+__device__ __forceinline__ void mma_add(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
 // d = a b.
 __device__ __forceinline__ void mma_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
@@ -217,6 +223,10 @@ __device__ __forceinline__ void load_scales(const uint8_t* p, float (&s)[D / 32]
   }
 }
 
+// Ranges that R slots are cut into: at least one slot per warp before another CTA joins in.
+__device__ __forceinline__ int ranges_of(long long R) {
+  return static_cast<int>(min(static_cast<long long>(gridDim.x), (R + kWarps - 1) / kWarps));
+}
 // First slot of CTA c's range, and the CTA of a slot, for R slots in N ranges.
 __device__ __forceinline__ long long range_of(long long R, int N, int c) { return R * c / N; }
 __device__ __forceinline__ int cta_of(long long R, int N, long long x) {
@@ -235,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
   float* sm_fm = reinterpret_cast<float*>(smem + S::FIN);       // [8] reference, then
   float* sm_fl = sm_fm + 8;                                     // [8] sum of the merged row
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::BAR);
-  long long* sm_total = reinterpret_cast<long long*>(smem + S::MISC);        // [0] R, [1] row0 of the start
+  long long* sm_total = reinterpret_cast<long long*>(smem + S::MISC);        // [0] R, [1] first slot of the range, counted from the start of *sm_start
   int* sm_start = reinterpret_cast<int*>(smem + S::MISC + 16);               // b of the start
   int* sm_ticket = sm_start + 1;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -253,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
   const int per = (a.B + kThreads - 1) / kThreads;
   const int bt0 = tid * per, bt1 = min(bt0 + per, a.B);
   long long mine = 0;
-  for (int b = bt0; b < bt1; ++b) mine += live_of(a, b, fa).slots;
+  for (int b = bt0; b < bt1; ++b) mine += slots_of(live_of(a, b, fa));
   mine *= a.Hkv;
   long long incl = mine;
 #pragma unroll
@@ -271,8 +281,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
     if (w < warp) before += x;
     R += x;
   }
-  // At least one slot per warp before another CTA joins in.
-  const int N = static_cast<int>(min(static_cast<long long>(gridDim.x), (R + kWarps - 1) / kWarps));
+  const int N = ranges_of(R);
   const int cta = blockIdx.x;
   const bool works = cta < N;
   const long long R0 = works ? range_of(R, N, cta) : 0, R1 = works ? range_of(R, N, cta + 1) : 0;
@@ -280,49 +289,57 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
     long long at = before;
     int b = bt0;
     for (;; ++b) {
-      const long long n = static_cast<long long>(live_of(a, b, fa).slots) * a.Hkv;
+      const long long n = static_cast<long long>(slots_of(live_of(a, b, fa))) * a.Hkv;
       if (R0 < at + n) break;
       at += n;
     }
     *sm_start = b;
-    sm_total[1] = at;
+    sm_total[0] = R;
+    sm_total[1] = R0 - at;
   }
   __syncthreads();
 
   const int g = lane >> 2, t = lane & 3;
 
   const Unpack um = unpack_masks();
-  const float sl2 = a.scale * 1.4426950408889634f, inv_sl2 = 1.f / sl2;
-  Walk w = {};
+  const float sl2 = a.scale * 1.4426950408889634f;
+  // The position in the range: row w, of which `done` slots are behind us, at
+  // slot `pos` of the CTA's `len`.
+  Row w = {};
+  uint32_t done = 0, pos = 0;
+  const uint32_t len = static_cast<uint32_t>(R1 - R0);
   if (works) {
     w.b = *sm_start;
-    w.v = live_of(a, w.b, fa);
-    const long long at = sm_total[1];
-    w.g = static_cast<int>((R0 - at) / w.v.slots);
-    w.row0 = at + static_cast<long long>(w.g) * w.v.slots;
+    w.slots = slots_of(live_of(a, w.b, fa));
+    w.g = static_cast<int>(sm_total[1] / w.slots);
+    done = static_cast<uint32_t>(sm_total[1] % w.slots);
   }
   // ---- the warp's stream of slots ---------------------------------------------
   // Slot n of the warp is number warp + kWarps n of the CTA's range and goes
   // to stage n mod kDepth of the warp's ring.
   uint8_t* ring = smem + warp * kDepth * 2 * L::BYTES;
   uint64_t* bars = full + warp * kDepth;
-  const long long left = R1 - R0 - warp;
-  const uint32_t total = left > 0 ? static_cast<uint32_t>((left + kWarps - 1) / kWarps) : 0u;
+  const uint32_t total = (len + kWarps - 1 - warp) / kWarps;
   uint32_t taken = 0;          // slots consumed
   uint32_t src = kNoRecord;    // lane's record of the current 16 pairs (index into the pool), or none
-  uint32_t missing = 0;        // two bits per stage: no such record
+  uint32_t joined = 0;         // bit 2 i: the records of the i-th of them stand side by side
+  uint32_t missing = 0;        // two bits per pair in flight, the oldest lowest: no such record
   bool ok = true;
-  auto fill = [&](uint32_t n) {
+  auto fill = [&](uint32_t n, int place) {
     if ((n & 15u) == 0) {      // places of pairs n .. n + 15
       src = kNoRecord;
       const uint32_t nl = n + (lane >> 1);
       if (nl < total) {
-        const long long x = R0 + warp + static_cast<long long>(kWarps) * nl;
-        Walk t = w;
-        while (x >= t.row0 + t.v.slots) next_row(a, fa, t);
-        const int k = 2 * static_cast<int>(x - t.row0) + (lane & 1);
-        if (k < t.v.count) {
-          const int rec = k < t.v.head ? k : t.v.tail + (k - t.v.head);
+        uint32_t x = done + (warp + kWarps * nl - pos);          // counted from the row's start
+        Row t = w;
+        while (x >= t.slots) {
+          x -= t.slots;
+          next_row(a, fa, t);
+        }
+        const int k = 2 * static_cast<int>(x) + (lane & 1);
+        const Live v = live_of(a, t.b, fa);
+        if (k < v.count) {
+          const int rec = k < v.head ? k : v.tail + (k - v.head);
           const int recs = a.page_size / kQ4Rec, lp = rec / recs;
           const int page = a.page_table[static_cast<size_t>(t.b) * a.max_pages + lp];
           if (page >= 0 && page < a.num_pages)
@@ -332,33 +349,31 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
         }
       }
       __syncwarp();
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, src, 1);
+      joined = __ballot_sync(0xffffffffu, src != kNoRecord && other == src + 1 && other != kNoRecord);
     }
-    const uint32_t i0 = __shfl_sync(0xffffffffu, src, (2 * n) & 31u);
-    const uint32_t i1 = __shfl_sync(0xffffffffu, src, (2 * n + 1) & 31u);
-    const uint32_t stage = n & (kDepth - 1);
-    const uint32_t none = (i0 == kNoRecord ? 1u : 0u) | (i1 == kNoRecord ? 2u : 0u);
-    missing = (missing & ~(3u << (2 * stage))) | (none << (2 * stage));
-    if (lane == 0) {
-      uint8_t* dst = ring + stage * 2 * L::BYTES;
-      const uint8_t* from = a.pool + static_cast<size_t>(i0) * L::BYTES;
-      if (none == 0) {
+    const uint32_t stage = n & (kDepth - 1), i = (2 * n) & 31u;
+    const uint32_t i0 = __shfl_sync(0xffffffffu, src, i);
+    uint8_t* dst = ring + stage * 2 * L::BYTES;
+    if (joined >> i & 1u) {
+      if (lane == 0) {
         mbar_arrive_expect_tx(bars + stage, 2 * L::BYTES);
-        if (i1 == i0 + 1) {
-          bulk_load(dst, from, 2 * L::BYTES, bars + stage);
-        } else {
-          bulk_load(dst, from, L::BYTES, bars + stage);
+        bulk_load(dst, a.pool + static_cast<size_t>(i0) * L::BYTES, 2 * L::BYTES, bars + stage);
+      }
+    } else {
+      const uint32_t i1 = __shfl_sync(0xffffffffu, src, i + 1);
+      const uint32_t none = (i0 == kNoRecord ? 1u : 0u) | (i1 == kNoRecord ? 2u : 0u);
+      missing |= none << (2 * place);
+      if (lane == 0) {
+        if (none == 3) mbar_arrive(bars + stage);
+        else mbar_arrive_expect_tx(bars + stage, none ? L::BYTES : 2 * L::BYTES);
+        if (!(none & 1u)) bulk_load(dst, a.pool + static_cast<size_t>(i0) * L::BYTES, L::BYTES, bars + stage);
+        if (!(none & 2u))
           bulk_load(dst + L::BYTES, a.pool + static_cast<size_t>(i1) * L::BYTES, L::BYTES, bars + stage);
-        }
-      } else if (none == 3) {
-        mbar_arrive(bars + stage);
-      } else {
-        mbar_arrive_expect_tx(bars + stage, L::BYTES);
-        if (none == 2) bulk_load(dst, from, L::BYTES, bars + stage);
-        else bulk_load(dst + L::BYTES, a.pool + static_cast<size_t>(i1) * L::BYTES, L::BYTES, bars + stage);
       }
     }
   };
-  for (uint32_t n = 0; n < kDepth && n < total; ++n) fill(n);
+  for (uint32_t n = 0; n < kDepth && n < total; ++n) fill(n, n);
 
   // Sequences with no live token: zero output, lse -inf.
   for (int b = cta; b < a.B; b += gridDim.x) {
@@ -373,14 +388,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
     if (a.lse)
       for (int i = tid; i < a.Hq; i += kThreads) a.lse[static_cast<size_t>(b) * a.Hq + i] = -INFINITY;
   }
-  float4* part = reinterpret_cast<float4*>(a.part);              // [2 gridDim][PART4], then m, l [..][8]
-  float* part_m = a.part + static_cast<size_t>(2) * gridDim.x * S::PART4 * 4;
-  float* part_l = part_m + 2 * gridDim.x * 8;
 
-  for (long long at = R0; at < R1;) {
-    const long long row1 = w.row0 + w.v.pairs;
-    const long long end = min(w.row0 + w.v.slots, R1);
-    const size_t head0 = static_cast<size_t>(w.b) * a.Hq + w.g * G;   // the group's first query head
+  while (pos < len) {
+    const uint32_t pairs = w.slots - kRowCost;
+    const uint32_t until = min(w.slots, done + (len - pos));       // of the row, in this range
+    const uint32_t head0 = static_cast<uint32_t>(w.b) * a.Hq + w.g * G;   // the group's first query head
 
     // Query operands: lane 4 g + t holds head g, channels 32 i + 8 t + e.  And
     // -24 times the head's group sums, cut into three bf16 numbers, as the
@@ -393,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
 #pragma unroll
       for (int i = 0; i < GR; ++i) {
         uint4 v = {0, 0, 0, 0};
-        if (g < G) v = *reinterpret_cast<const uint4*>(a.q + (head0 + g) * D + 32 * i + 8 * t);
+        if (g < G) v = *reinterpret_cast<const uint4*>(a.q + static_cast<size_t>(head0 + g) * D + 32 * i + 8 * t);
         qf[i][0] = v.x;
         qf[i][1] = v.y;
         qf[i][2] = v.z;
@@ -428,8 +440,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
     }
 
     // The next row's query, for when it is its turn.
-    if (end < R1 && lane < G * D / 64 && head0 + 2 * G <= static_cast<size_t>(a.B) * a.Hq)
-      asm volatile("prefetch.global.L1 [%0];" ::"l"(a.q + (head0 + G) * D + lane * 64));
+    if (pos + (until - done) < len && lane < G * D / 64 && head0 + 2 * G <= static_cast<uint32_t>(a.B) * a.Hq)
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(a.q + static_cast<size_t>(head0 + G) * D + lane * 64));
 
     float o[NT][4];
 #pragma unroll
@@ -439,14 +451,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
     float th0 = kLowest, th1 = kLowest;        // a score (before the scale) above it moves the reference
 
     // The warp takes every kWarps-th slot of the CTA's range.
-    const int skip = (warp + kWarps - static_cast<int>((at - R0) % kWarps)) % kWarps;
-    const int j_end = static_cast<int>(end - w.row0);
-    for (int j = static_cast<int>(at - w.row0) + skip; j < j_end; j += kWarps, ++taken) {
+    const uint32_t skip = (warp - pos) % kWarps;
+    int plain1, plain2, plain3;
+    {
+      const Live v = live_of(a, w.b, fa);
+      plain1 = v.plain1;
+      plain2 = v.plain2;
+      plain3 = v.plain3;
+    }
+    for (int j = static_cast<int>(done + skip); j < static_cast<int>(until) && ok; j += kWarps, ++taken) {
       const uint32_t stage = taken & (kDepth - 1), parity = (taken / kDepth) & 1u;
-      const uint32_t none = missing >> (2 * stage) & 3u;
-      if (!ok) continue;
+      const uint32_t none = missing & 3u;
+      missing >>= 2;
       if (none == 3u) {        // an empty slot, or no valid page: nothing was copied
-        if (taken + kDepth < total) fill(taken + kDepth);
+        if (taken + kDepth < total) fill(taken + kDepth, kDepth - 1);
         continue;
       }
       if (!__all_sync(0xffffffffu, mbar_try_wait(bars + stage, parity))) {
@@ -455,11 +473,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
           raise_error(a.st.err, DEV_ERR_TIMEOUT);
           for (uint32_t n = taken; n < total && n < taken + kDepth; ++n)
             mbar_drain(bars + (n & (kDepth - 1)), (n / kDepth) & 1u);
-          continue;
+          break;
         }
       }
       const uint8_t* rec = ring + stage * 2 * L::BYTES;
 
+      uint32_t v0[2][GR], v1[2][GR], sv0[2], sv1[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint8_t* p = rec + r * L::BYTES;
+        load_words<D>(p + L::VC + lane * (D / 8), v0[r]);
+        load_words<D>(p + L::VC + 4 * D + lane * (D / 8), v1[r]);
+        const uint8_t* vs = p + L::VS + (g * (D / 8) / 32) * 32 + 4 * t;
+        sv0[r] = *reinterpret_cast<const uint32_t*>(vs);
+        sv1[r] = *reinterpret_cast<const uint32_t*>(vs + 16);
+      }
       float x[2][4];           // scores: tokens g, g + 8, heads 2 t, 2 t + 1
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -488,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
           {
             const uint32_t af[4] = {k_pair<2>(k0[i], um), k_pair<2>(k1[i], um), k_pair<3>(k0[i], um),
                                     k_pair<3>(k1[i], um)};
-            mma_bf16_16816(acc, af, qf[i][2], qf[i][3]);
+            mma_add(acc, af, qf[i][2], qf[i][3]);
           }
           x[r][0] = fmaf(s0[i], acc[0], x[r][0]);
           x[r][1] = fmaf(s0[i], acc[1], x[r][1]);
@@ -496,28 +524,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
           x[r][3] = fmaf(s1[i], acc[3], x[r][3]);
         }
       }
-      uint32_t v0[2][GR], v1[2][GR], sv0[2], sv1[2];
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const uint8_t* p = rec + r * L::BYTES;
-        load_words<D>(p + L::VC + lane * (D / 8), v0[r]);
-        load_words<D>(p + L::VC + 4 * D + lane * (D / 8), v1[r]);
-        const uint8_t* vs = p + L::VS + (g * (D / 8) / 32) * 32 + 4 * t;
-        sv0[r] = *reinterpret_cast<const uint32_t*>(vs);
-        sv1[r] = *reinterpret_cast<const uint32_t*>(vs + 16);
-      }
       __syncwarp();
-      if (taken + kDepth < total) fill(taken + kDepth);
+      if (taken + kDepth < total) fill(taken + kDepth, kDepth - 1);
       // A pair at the end of the sequence or of the sink or window, or with a
       // missing page: tokens that are not live score -inf, and their values
       // count as zero whatever bytes stand there.
-      if (none != 0 || !(j < w.v.plain1 || (j >= w.v.plain2 && j < w.v.plain3))) {
+      if (none != 0 || !(j < plain1 || (j >= plain2 && j < plain3))) {
+        const Live v = live_of(a, w.b, fa);
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const int k = 2 * j + r;
-          const int u0 = (k < w.v.head ? k : w.v.tail + (k - w.v.head)) * kQ4Rec;
+          const int u0 = (k < v.head ? k : v.tail + (k - v.head)) * kQ4Rec;
           const bool there = !(none >> r & 1u);
-          auto live = [&](int u) { return there && u < w.v.s && (u < w.v.n_sink || u >= w.v.win); };
+          auto live = [&](int u) { return there && u < v.s && (u < v.n_sink || u >= v.win); };
           if (!live(u0 + g)) x[r][0] = x[r][1] = -INFINITY;
           if (!live(u0 + g + 8)) x[r][2] = x[r][3] = -INFINITY;
           if (!live(u0 + 2 * t)) sv0[r] &= 0xffff0000u;
@@ -540,8 +559,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
         const float f0 = ex2(m0 - n0), f1 = ex2(m1 - n1);
         m0 = n0;
         m1 = n1;
-        th0 = (n0 + kGrow) * inv_sl2;
-        th1 = (n1 + kGrow) * inv_sl2;
+        th0 = (n0 + kGrow) / sl2;
+        th1 = (n1 + kGrow) / sl2;
         l0 *= f0;
         l1 *= f1;
 #pragma unroll
@@ -569,21 +588,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
             const uint32_t af[4] = {
                 fma_bf16x2(v_pair<0>(a0, um), sv0[r], n0), fma_bf16x2(v_pair<1>(a0, um), sv0[r], n0),
                 fma_bf16x2(v_pair<0>(a1, um), sv1[r], n1), fma_bf16x2(v_pair<1>(a1, um), sv1[r], n1)};
-            mma_bf16_16816(o[2 * i], af, b0, b1);
+            mma_add(o[2 * i], af, b0, b1);
           }
           {
             const uint32_t af[4] = {
                 fma_bf16x2(v_pair<2>(a0, um), sv0[r], n0), fma_bf16x2(v_pair<3>(a0, um), sv0[r], n0),
                 fma_bf16x2(v_pair<2>(a1, um), sv1[r], n1), fma_bf16x2(v_pair<3>(a1, um), sv1[r], n1)};
-            mma_bf16_16816(o[2 * i + 1], af, b0, b1);
+            mma_add(o[2 * i + 1], af, b0, b1);
           }
         }
       }
     }
 
-    if (at >= row1) {          // the range begins in the row's empty slots
-      at = end;
-      if (at < R1) next_row(a, fa, w);
+    const bool begins = done == 0, ends = until >= pairs;
+    if (done >= pairs) {       // the range began in the row's empty slots
+      pos += until - done;
+      done = 0;
+      if (pos < len) next_row(a, fa, w);
       continue;
     }
     // ---- merge the warps --------------------------------------------------
@@ -602,8 +623,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
       sm_l[warp * 8 + 2 * t + 1] = l1;
     }
     const bool fine = named_bar_and(1, kThreads, ok);
-    const bool whole = at == w.row0 && end >= row1;
-    const int slot = 2 * cta + (at == w.row0 ? 1 : 0);
+    const bool whole = begins && ends;
+    const int slot = 2 * cta + (begins ? 1 : 0);
+    float4* part = reinterpret_cast<float4*>(a.part);            // [2 gridDim][PART4], then m, l [..][8]
+    float* part_m = a.part + static_cast<size_t>(2) * gridDim.x * S::PART4 * 4;
+    float* part_l = part_m + 2 * gridDim.x * 8;
     for (int i = tid; i < S::PART4; i += kThreads) {
       const int h = 2 * (i & 3), gi = (i & 31) >> 2, m = i >> 5;
       if (h >= G) continue;
@@ -632,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
       }
       if (whole) {
         const float i0 = ls0 != 0.f ? 1.f / ls0 : 0.f, i1 = ls1 != 0.f ? 1.f / ls1 : 0.f;
-        uint16_t* out = a.o + (head0 + h) * D + gi * (D / 8) + 2 * m;
+        uint16_t* out = a.o + static_cast<size_t>(head0 + h) * D + gi * (D / 8) + 2 * m;
         *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(r.x * i0, r.z * i0);
         if (h + 1 < G) *reinterpret_cast<uint32_t*>(out + D) = pack_bf16x2(r.y * i1, r.w * i1);
         if (a.lse && m == 0 && gi == 0) {
@@ -651,7 +675,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
     }
     if (!whole) {
       // ---- merge the CTAs of a row: the one that comes last ----------------
-      const int first = cta_of(R, N, w.row0), last = cta_of(R, N, row1 - 1);
+      const long long Rt = sm_total[0];
+      const int Nt = ranges_of(Rt);
+      const long long row0 = range_of(Rt, Nt, cta) + pos - done;
+      const int first = cta_of(Rt, Nt, row0), last = cta_of(Rt, Nt, row0 + pairs - 1);
       __threadfence();
       named_bar_sync(1, kThreads);
       if (tid == 0) {
@@ -712,14 +739,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
             r.w = fmaf(w1, v.w, r.w);
           }
           const float i0 = sm_fl[h], i1 = sm_fl[h + 1];
-          uint16_t* out = a.o + (head0 + h) * D + gi * (D / 8) + 2 * m;
+          uint16_t* out = a.o + static_cast<size_t>(head0 + h) * D + gi * (D / 8) + 2 * m;
           *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(r.x * i0, r.z * i0);
           if (h + 1 < G) *reinterpret_cast<uint32_t*>(out + D) = pack_bf16x2(r.y * i1, r.w * i1);
         }
       }
     }
-    at = end;
-    if (at < R1) {
+    pos += until - done;
+    done = 0;
+    if (pos < len) {
       next_row(a, fa, w);
       named_bar_sync(1, kThreads);      // the merge buffer is free again
     }

@@ -98,6 +98,8 @@ def header_symbols(path: str = HEADER):
 def lib() -> ctypes.CDLL:
     """Load libflux.so (built in-tree by sparse_attention_flux_b200.build)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -129,7 +131,6 @@ def _stream(stream=None):
 
 
 def _need(t, dtype, name, device=None):
-    import torch
     if t is None:
         return
     if not t.is_cuda:
@@ -142,22 +143,32 @@ def _need(t, dtype, name, device=None):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
-def _need_rows(t, name, device):
-    """A [N, H, d] bf16 view whose heads are contiguous within a token (any token stride)."""
-    import torch
-    if t.dtype != torch.bfloat16:
-        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dim() != 3:
+# The calls of a decode step are made once per layer and token, so these check and marshal in
+# one go: about 0.4 us an argument, the torch calls that say nothing new left out.
+def _at(t, dtype, name, ctx):
+    """Address of a contiguous tensor of that type on the ctx's device (None: none)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.get_device() != ctx._index or not t.is_contiguous():
+        _need(t, dtype, name, ctx.device)
+    return t.data_ptr()
+
+
+def _rows_at(t, name, ctx):
+    """Address, token stride and shape of a [N, H, d] bf16 view whose heads are contiguous within
+    a token (any token stride)."""
+    if t.dtype is not ctx._bf16:
+        raise ValueError(f"{name} must be {ctx._bf16}, got {t.dtype}")
+    if t.get_device() != ctx._index:
+        raise ValueError(f"{name} is on {t.device}, expected {ctx.device}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3:
         raise ValueError(f"{name} must be [N, H, d]")
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+    N, H, d = shape
+    if stride[2] != 1 or (H > 1 and stride[1] != d):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-
-
-def _row_stride(t):
     # a single token's stride says nothing (torch leaves any number there)
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return t.data_ptr(), stride[0] if N > 1 else H * d, shape
 
 
 def kv_q4_pool_shape(num_pages: int, Hkv: int, page_size: int, d: int):
@@ -175,6 +186,10 @@ class Context:
     def __init__(self, device: int = 0, workspace_bytes: int = 0):
         import torch
         self.device = torch.device("cuda", device)
+        self._index = device
+        self._bf16, self._f32, self._u8 = torch.bfloat16, torch.float32, torch.uint8
+        self._i32, self._i64 = torch.int32, torch.int64
+        self._raw_stream = torch._C._cuda_getCurrentRawStream
         h = ctypes.c_void_p()
         _check(lib().flux_ctx_create(ctypes.byref(h), device, workspace_bytes))
         self._h = h
@@ -455,13 +470,16 @@ class Context:
                                              1 if compact else 0, float(scale), _stream(stream)))
 
     # ------------------------------------------------------------------ paged 4-bit KV cache
+    def _on(self, stream):
+        return self._raw_stream(self._index) if stream is None else stream.cuda_stream
+
     def _pool(self, kv_pool, Hkv, d):
-        """(num_pages, page_size) of a cache tensor made with kv_q4_pool_shape."""
-        import torch
-        _need(kv_pool, torch.uint8, "kv_pool", self.device)
-        if kv_pool.dim() != 4 or kv_pool.shape[1] != Hkv or kv_pool.shape[3] != 18 * d:
+        """(address, num_pages, page_size) of a cache tensor made with kv_q4_pool_shape."""
+        at = _at(kv_pool, self._u8, "kv_pool", self)
+        shape = kv_pool.shape
+        if len(shape) != 4 or shape[1] != (Hkv or shape[1]) or shape[3] != 18 * d:
             raise ValueError("kv_pool must be [num_pages, Hkv, page_size / 16, 18 * d]")
-        return kv_pool.shape[0], kv_pool.shape[2] * 16
+        return at, shape[0], shape[2] * 16
 
     def decode_q4_workspace_bytes(self, d: int) -> int:
         n = ctypes.c_size_t()
@@ -474,109 +492,101 @@ class Context:
         """Block tables, slot map and positions of the step in which the requests grow from
         old_lens to new_lens; pages come from free_pages[cursor:].  window_pages > 0: a ring of
         sink + window pages per request (SA layers)."""
-        import torch
-        for n_, t in (("old_lens", old_lens), ("new_lens", new_lens), ("free_pages", free_pages),
-                      ("cursor", cursor), ("cursor_out", cursor_out), ("page_table", page_table),
-                      ("positions", positions), ("cu_new", cu_new)):
-            _need(t, torch.int32, n_, self.device)
-        _need(slots, torch.int64, "slots", self.device)
-        B = old_lens.numel()
-        if page_table.dim() != 2 or page_table.shape[0] != B or new_lens.numel() != B:
+        i32 = self._i32
+        args = [_at(t, i32, n_, self) for n_, t in (
+            ("old_lens", old_lens), ("new_lens", new_lens), ("free_pages", free_pages),
+            ("cursor", cursor), ("cursor_out", cursor_out), ("page_table", page_table),
+            ("positions", positions), ("cu_new", cu_new))]
+        slots_at = _at(slots, self._i64, "slots", self)
+        B, n_slots, table = old_lens.numel(), slots.numel(), page_table.shape
+        if len(table) != 2 or table[0] != B or new_lens.numel() != B:
             raise ValueError("old_lens / new_lens / page_table shapes are inconsistent")
-        if positions.numel() != slots.numel() or cursor.numel() < 1 or cursor_out.numel() < 1:
+        if positions.numel() != n_slots or cursor.numel() < 1 or cursor_out.numel() < 1:
             raise ValueError("slots / positions / cursor shapes are inconsistent")
         if cu_new is not None and cu_new.numel() < B + 1:
             raise ValueError("cu_new needs B + 1 entries")
         _check(lib().flux_build_page_table(
-            self._h, _ptr(old_lens), _ptr(new_lens), B, page_size, sink_pages, window_pages,
-            _ptr(free_pages), free_pages.numel(), _ptr(cursor), _ptr(cursor_out), _ptr(page_table),
-            page_table.shape[1], _ptr(slots), _ptr(positions), slots.numel(), _ptr(cu_new),
-            _stream(stream)))
+            self._h, args[0], args[1], B, page_size, sink_pages, window_pages, args[2],
+            free_pages.numel(), args[3], args[4], args[5], table[1], slots_at, args[6], n_slots,
+            args[7], self._on(stream)))
 
     def qk_norm_rope(self, q, k, q_out, k_out, positions, inv_freq, q_weight=None, k_weight=None,
                      eps: float = 1e-6, interleaved: bool = False, stream=None):
         """Per-head RMS norm of q [N, Hq, d] and k [N, Hkv, d] (weights [d]; none: no norm) and
         the rotation by positions * inv_freq of their first 2 * len(inv_freq) channels.  q and k
         may be views of a packed projection; an output may be its input."""
-        import torch
-        for n_, t in (("q", q), ("k", k), ("q_out", q_out), ("k_out", k_out)):
-            _need_rows(t, n_, self.device)
-        _need(positions, torch.int32, "positions", self.device)
-        _need(inv_freq, torch.float32, "inv_freq", self.device)
-        _need(q_weight, torch.bfloat16, "q_weight", self.device)
-        _need(k_weight, torch.bfloat16, "k_weight", self.device)
-        N, Hq, d = q.shape
-        Hkv = k.shape[1]
-        if k.shape != (N, Hkv, d) or q_out.shape != q.shape or k_out.shape != k.shape \
+        q_at, q_stride, q_shape = _rows_at(q, "q", self)
+        k_at, k_stride, k_shape = _rows_at(k, "k", self)
+        qo_at, qo_stride, qo_shape = _rows_at(q_out, "q_out", self)
+        ko_at, ko_stride, ko_shape = _rows_at(k_out, "k_out", self)
+        pos_at = _at(positions, self._i32, "positions", self)
+        freq_at = _at(inv_freq, self._f32, "inv_freq", self)
+        qw_at = _at(q_weight, self._bf16, "q_weight", self)
+        kw_at = _at(k_weight, self._bf16, "k_weight", self)
+        N, Hq, d = q_shape
+        Hkv = k_shape[1]
+        if k_shape[0] != N or k_shape[2] != d or qo_shape != q_shape or ko_shape != k_shape \
                 or positions.numel() != N:
             raise ValueError("q / k / output / positions shapes are inconsistent")
         for w in (q_weight, k_weight):
             if w is not None and w.numel() != d:
                 raise ValueError("norm weights must have head_dim entries")
         _check(lib().flux_qk_norm_rope(
-            self._h, _ptr(q), _row_stride(q), _ptr(k), _row_stride(k), _ptr(q_out),
-            _row_stride(q_out), _ptr(k_out), _row_stride(k_out), N, Hq, Hkv, d, _ptr(q_weight),
-            _ptr(k_weight), float(eps), _ptr(positions), _ptr(inv_freq), 2 * inv_freq.numel(),
-            1 if interleaved else 0, _stream(stream)))
+            self._h, q_at, q_stride, k_at, k_stride, qo_at, qo_stride, ko_at, ko_stride, N, Hq,
+            Hkv, d, qw_at, kw_at, eps, pos_at, freq_at, 2 * inv_freq.numel(),
+            1 if interleaved else 0, self._on(stream)))
 
     def kv_write_q4(self, k_src, v_src, slots, kv_pool, stream=None):
         """Quantise k_src, v_src [N, Hkv, d] (views of a packed projection may do) into the
         slots of a paged 4-bit cache; negative slots are skipped."""
-        import torch
-        _need_rows(k_src, "k_src", self.device)
-        _need_rows(v_src, "v_src", self.device)
-        _need(slots, torch.int64, "slots", self.device)
-        N, Hkv, d = k_src.shape
-        if v_src.shape != k_src.shape or slots.numel() != N:
+        k_at, k_stride, shape = _rows_at(k_src, "k_src", self)
+        v_at, v_stride, v_shape = _rows_at(v_src, "v_src", self)
+        slots_at = _at(slots, self._i64, "slots", self)
+        N, Hkv, d = shape
+        if v_shape != shape or slots.numel() != N:
             raise ValueError("k_src / v_src / slots shapes are inconsistent")
-        num_pages, page_size = self._pool(kv_pool, Hkv, d)
-        _check(lib().flux_kv_write_q4(self._h, _ptr(k_src), _row_stride(k_src), _ptr(v_src),
-                                      _row_stride(v_src), _ptr(slots), N, Hkv, d, _ptr(kv_pool),
-                                      num_pages, page_size, _stream(stream)))
+        pool_at, num_pages, page_size = self._pool(kv_pool, Hkv, d)
+        _check(lib().flux_kv_write_q4(self._h, k_at, k_stride, v_at, v_stride, slots_at, N, Hkv, d,
+                                      pool_at, num_pages, page_size, self._on(stream)))
 
     def kv_read_q4(self, kv_pool, slots, k_dst, v_dst, stream=None):
         """The stored values of the slots as bf16 rows k_dst, v_dst [N, Hkv, d]; rows of
         negative slots are left as they were."""
-        import torch
-        _need(k_dst, torch.bfloat16, "k_dst", self.device)
-        _need(v_dst, torch.bfloat16, "v_dst", self.device)
-        _need(slots, torch.int64, "slots", self.device)
-        if k_dst.dim() != 3 or v_dst.shape != k_dst.shape or slots.numel() != k_dst.shape[0]:
+        k_at = _at(k_dst, self._bf16, "k_dst", self)
+        v_at = _at(v_dst, self._bf16, "v_dst", self)
+        slots_at = _at(slots, self._i64, "slots", self)
+        shape = k_dst.shape
+        if len(shape) != 3 or v_dst.shape != shape or slots.numel() != shape[0]:
             raise ValueError("k_dst / v_dst / slots shapes are inconsistent")
-        N, Hkv, d = k_dst.shape
-        num_pages, page_size = self._pool(kv_pool, Hkv, d)
-        _check(lib().flux_kv_read_q4(self._h, _ptr(kv_pool), num_pages, page_size, _ptr(slots), N,
-                                     Hkv, d, _ptr(k_dst), _ptr(v_dst), _stream(stream)))
+        N, Hkv, d = shape
+        pool_at, num_pages, page_size = self._pool(kv_pool, Hkv, d)
+        _check(lib().flux_kv_read_q4(self._h, pool_at, num_pages, page_size, slots_at, N, Hkv, d,
+                                     k_at, v_at, self._on(stream)))
 
     def attn_decode_q4(self, q, kv_pool, page_table, seqlens, o, scale: float, layer_mode=None,
                        layer: int = 0, sink_blocks: int = 1, window_blocks: int = 16,
                        block: int = 128, lse=None, stream=None):
         """attn_decode over a paged 4-bit cache: token u of sequence b is in page
         page_table[b, u // page_size] of kv_pool."""
-        import torch
-        _need(q, torch.bfloat16, "q", self.device)
-        _need(o, torch.bfloat16, "o", self.device)
-        _need(page_table, torch.int32, "page_table", self.device)
-        _need(seqlens, torch.int32, "seqlens", self.device)
-        _need(lse, torch.float32, "lse", self.device)
-        _need(layer_mode, torch.uint8, "layer_mode", self.device)
-        B, Hq, d = q.shape
-        if kv_pool.dim() != 4:
-            raise ValueError("kv_pool must be [num_pages, Hkv, page_size / 16, 18 * d]")
-        Hkv = kv_pool.shape[1]
-        num_pages, page_size = self._pool(kv_pool, Hkv, d)
-        if page_table.dim() != 2 or page_table.shape[0] != B or seqlens.numel() != B \
-                or o.shape != q.shape:
+        q_at = _at(q, self._bf16, "q", self)
+        o_at = _at(o, self._bf16, "o", self)
+        table_at = _at(page_table, self._i32, "page_table", self)
+        lens_at = _at(seqlens, self._i32, "seqlens", self)
+        lse_at = _at(lse, self._f32, "lse", self)
+        mode_at = _at(layer_mode, self._u8, "layer_mode", self)
+        shape, table = q.shape, page_table.shape
+        B, Hq, d = shape
+        pool_at, num_pages, page_size = self._pool(kv_pool, None, d)
+        if len(table) != 2 or table[0] != B or seqlens.numel() != B or o.shape != shape:
             raise ValueError("q / page_table / seqlens / o shapes are inconsistent")
         if lse is not None and lse.numel() < B * Hq:
             raise ValueError("lse too small")
         if layer_mode is not None and layer >= layer_mode.numel():
             raise ValueError("layer is outside layer_mode")
-        _check(lib().flux_attn_decode_q4(self._h, _ptr(q), _ptr(kv_pool), num_pages, page_size,
-                                         _ptr(page_table), page_table.shape[1], _ptr(seqlens),
-                                         _ptr(o), _ptr(lse), B, Hq, Hkv, d, _ptr(layer_mode),
-                                         layer, sink_blocks, window_blocks, block, float(scale),
-                                         _stream(stream)))
+        _check(lib().flux_attn_decode_q4(self._h, q_at, pool_at, num_pages, page_size, table_at,
+                                         table[1], lens_at, o_at, lse_at, B, Hq,
+                                         kv_pool.shape[1], d, mode_at, layer, sink_blocks,
+                                         window_blocks, block, scale, self._on(stream)))
 
 
 def attn_decode_noalloc(q, k_cache, v_cache, seqlens, o, scale: float, layer_mode=None,
