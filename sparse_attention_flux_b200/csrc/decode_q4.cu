@@ -6,16 +6,17 @@
 // is the unpacking, so the kernel is built to keep HBM busy with as few issued
 // instructions per record as possible.
 //
-// Work split.  The live records of all (sequence, kv head) rows, in pairs, are laid end to
-// end and cut into equal ranges, one per CTA (two CTAs per SM, one wave), so a
-// ragged batch loads every SM alike; a row counts kRowCost empty slots more
-// than its pairs, since its merge takes about as long (without them the CTA
-// that gets a batch's short requests, 45 rows, took 90 us of a 30 us call).  A CTA walks its range row by row; within
-// a row its warps take pairs in turn and merge at the row's
-// end in shared memory.  A row that crosses a range border (at most the first
-// and the last of a CTA) leaves a partial in the workspace; the CTA that
-// delivers a row's last partial (a ticket) merges them in range order, so the
-// result does not depend on timing.
+// Work split.  The live records of all (sequence, kv head) rows, in pairs, are
+// laid end to end and cut into equal ranges, one per CTA (two CTAs per SM, one
+// wave), so a ragged batch loads every SM alike.  A row counts kRowCost empty
+// slots more than its pairs for what it costs beside them; without any, the CTA
+// that got a batch's short requests, 45 rows of one or two pairs, took 90 us of
+// a call whose others ended after 25.  Where the rows are alike and few, each is
+// cut by itself instead.  A CTA walks its range row by row; within a row its
+// warps take pairs in turn and merge at the row's end in shared memory.  A row
+// that crosses a range border (at most the first and the last of a CTA) leaves a
+// partial in the workspace; the CTA that delivers a row's last partial (a
+// ticket) merges them in range order, so the result does not depend on timing.
 //
 // Stream.  Records are taken in pairs.  Each warp keeps a ring of two pairs in
 // shared memory, filled by bulk copies (one, when the page holds both records):
@@ -23,16 +24,23 @@
 // itself, so a full barrier per stage is all the synchronisation there is.  The
 // places of a warp's next 16 pairs are looked up at once, a lane each record.
 //
-// Arithmetic per record, one warp, warp MMAs (m16n8k16, bf16, fp32 sums):
+// Arithmetic per record, one warp, warp MMAs (m16n8k16, bf16, fp32 sums).  A
+// 4-bit field u = code + 8 that stands alone in the low byte of a bf16 number is
+// u times a power of two (exponent 0 or 1: the subnormals and the first normals
+// lie on one line), so an AND makes an operand, and one shift serves two pairs.
 //   S = K q^T: the 16 tokens are the rows, the group's query heads (up to 8)
-//     the columns.  A code's 4 bits are a bf16 mantissa's upper bits, so one
-//     AND-OR per pair makes operands 16 + u, u = code + 8; the products of one
-//     32-channel group are multiplied by the token's scale in fp32.  What the
-//     16 + 8 adds, 24 sum(q) per group, comes off by an MMA of the scales with
-//     it (in three bf16 pieces, 24 bits).
-//   O^T += V^T P^T: the lane's channels are the rows; (16 + u) s - 24 s is one
-//     packed fma and exactly the stored value.  P is rounded to bf16 for the
-//     MMA (the softmax sum keeps fp32 values) and turned by movmatrix.
+//     the columns.  The query is scaled by a power of two per head (exact) to
+//     meet the operands' 2^-133; the products of one 32-channel group are
+//     multiplied by the token's scale in fp32, and the 8 sum(q) that u adds per
+//     group comes off by an MMA of the scales with it (three bf16 pieces, 24
+//     bits).
+//   O^T += V^T P^T: the lane's channels are the rows; u s - 8 s is one packed
+//     fma with s brought up by 2^108, and exactly the stored value times 2^-25.
+//     P is rounded to bf16 for the MMA (the softmax sum keeps fp32 values) and
+//     turned by movmatrix.
+// Unpacking by shift and AND-OR into 16 + u instead, seven or eight operations
+// for four pairs where these take six and five: 249 us against 224 (16 x 65536
+// tokens, 8 kv heads, d 128).
 // The softmax runs against a reference that only grows when a score passes it
 // by 8 (in log2 units): p <= 2^8, and the common record needs no rescaling and
 // one vote.
@@ -46,7 +54,8 @@ constexpr int kWarps = 8;                   // per CTA; 16 per SM, 128 registers
 constexpr int kThreads = 32 * kWarps;
 constexpr int kDepth = 2;                   // ring stages of a warp, a pair of records each
 constexpr int kStages = kDepth * kWarps;
-constexpr int kRowCost = kWarps;            // what a row's merge costs, in pairs of the split (below)
+constexpr int kRowCost = 16;                // what a row costs beside its pairs, in pairs: a ragged batch of 16
+                                            // up to 32768 tokens took 37.5, 32.5, 32.4, 32.6 us with 8, 14, 20, 28
 constexpr uint32_t kNoRecord = 0xffffffffu;
 constexpr int kCtasPerSm = 2;
 constexpr float kGrow = 8.f;                // log2 growth of a score that is tolerated
@@ -62,10 +71,11 @@ struct Q4Smem {
   static constexpr int PART4 = NT * 32;                   // float4 per partial
   static constexpr int ACC = kWarps * PART4 * 16;
   static constexpr int ML = RING + ACC;                   // m, l [warp][8]
-  static constexpr int FIN = ML + 2 * kWarps * 8 * 4;     // weights and 1 / l of the final merge
-  static constexpr int BAR = FIN + 2 * 8 * 4;
+  static constexpr int FIN = ML + 2 * kWarps * 8 * 4;     // 1 / l of the final merge
+  static constexpr int BAR = FIN + 8 * 4;
   static constexpr int MISC = BAR + kStages * 8;          // start row, totals, ticket
-  static constexpr int BYTES = MISC + 64;
+  static constexpr int WHERE = MISC + 64;                 // where each warp is
+  static constexpr int BYTES = WHERE + kWarps * 32;
 };
 
 // The live records of one sequence: [0, head) and [tail, end) of its records;
@@ -109,24 +119,32 @@ __device__ __forceinline__ Live live_of(const DecodeQ4Launch& a, int b, bool fa)
   return v;
 }
 
-__device__ __forceinline__ int slots_of(const Live& v) { return v.pairs > 0 ? v.pairs + kRowCost : 0; }
+// How the rows are laid end to end: each row's pairs and some empty slots.
+// even == 0: a row has kRowCost empty slots; else every row has `even` slots.
+struct Plan {
+  uint32_t even;
+};
+__device__ __forceinline__ uint32_t slots_of(const Plan& p, uint32_t pairs) {
+  return pairs == 0 ? 0u : p.even ? p.even : pairs + kRowCost;
+}
 
-// Row (b, g) and its slots; rows without records are skipped.
+// Row (b, g), its pairs and its slots; rows without records are skipped.
 struct Row {
   int b, g;
-  uint32_t slots;
+  uint32_t pairs, slots;
 };
 
-__device__ __forceinline__ void next_row(const DecodeQ4Launch& a, bool fa, Row& w) {
+__device__ __forceinline__ void next_row(const DecodeQ4Launch& a, bool fa, const Plan& p, Row& w) {
   if (++w.g == a.Hkv) {
     w.g = 0;
     do {
       ++w.b;
       if (w.b >= a.B) {    // behind the last row: never reached while records remain
-        w.slots = 0xffffffffu;
+        w.pairs = w.slots = 0xffffffffu;
         return;
       }
-      w.slots = slots_of(live_of(a, w.b, fa));
+      w.pairs = live_of(a, w.b, fa).pairs;
+      w.slots = slots_of(p, w.pairs);
     } while (w.slots == 0);
   }
 }
@@ -158,6 +176,12 @@ __device__ __forceinline__ void mma_add(float (&d)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+  return r;
+}
+
 // d = a b.
 __device__ __forceinline__ void mma_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm(
@@ -167,31 +191,27 @@ __device__ __forceinline__ void mma_zero(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// (x & code) | base with both constants in registers: one LOP3.
-struct Unpack {
-  uint32_t code, base;
-};
-__device__ __forceinline__ Unpack unpack_masks() {
-  Unpack u;             // opaque to the compiler, which would fold them into two instructions
-  asm volatile("mov.u32 %0, 0x00780078;" : "=r"(u.code));   // the upper four mantissa bits of both halves
-  asm volatile("mov.u32 %0, 0x41804180;" : "=r"(u.base));   // 16.0, 16.0
-  return u;
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
 }
-__device__ __forceinline__ uint32_t and_or(uint32_t x, const Unpack& u) {
-  uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(x), "r"(u.code), "r"(u.base));
-  return r;
-}
-// Operand pairs of a K word (stored rotated left by 3): channels 2 i, 2 i + 1.
+
+// Two 4-bit fields, one of each 16-bit half.  A field alone at bits 0..3 (even I)
+// or 4..7 (odd I) is a bf16 number whose exponent is zero or one, and linear in u
+// through both: u 2^-133, or u 2^-129.
 template <int I>
-__device__ __forceinline__ uint32_t k_pair(uint32_t w, const Unpack& u) {
-  return and_or(I == 0 ? w : (I == 3 ? __funnelshift_r(w, w, 12) : w >> (4 * I)), u);
+__device__ __forceinline__ uint32_t fields(uint32_t y) {    // y: the word, or for I > 1 the word >> 8
+  return y & (I % 2 ? 0x00f000f0u : 0x000f000fu);
 }
-// Operand pairs of a V word: channel i of both tokens.
-template <int I>
-__device__ __forceinline__ uint32_t v_pair(uint32_t w, const Unpack& u) {
-  return and_or(I == 0 ? w << 3 : w >> (4 * I - 3), u);
-}
+// The values are brought up by S = scale 2^108 (odd fields: 2^104), so that the
+// operand (u - 8) scale 2^-25 is exact for every stored scale below 2^20; larger
+// ones, and NaN, take another way.
+constexpr uint32_t kUpEven = 0x75807580u, kUpOdd = 0x73807380u;    // 2^108, 2^104
+constexpr uint32_t kDown8 = 0xb480b480u;                            // -8 2^-25 = -2^-22
+constexpr uint32_t kLarge = 0x36803680u;        // carries a half >= 2^20 into its upper bit
+constexpr float kValueUnit = 33554432.f;        // 2^25
 
 template <int D>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[D / 32]) {
@@ -223,14 +243,27 @@ __device__ __forceinline__ void load_scales(const uint8_t* p, float (&s)[D / 32]
   }
 }
 
-// Ranges that R slots are cut into: at least one slot per warp before another CTA joins in.
-__device__ __forceinline__ int ranges_of(long long R) {
-  return static_cast<int>(min(static_cast<long long>(gridDim.x), (R + kWarps - 1) / kWarps));
+__device__ __forceinline__ long long div_of(long long x, long long y) {
+  return (static_cast<unsigned long long>(x) | static_cast<unsigned long long>(y)) >> 32
+             ? x / y
+             : static_cast<long long>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y));
 }
-// First slot of CTA c's range, and the CTA of a slot, for R slots in N ranges.
-__device__ __forceinline__ long long range_of(long long R, int N, int c) { return R * c / N; }
-__device__ __forceinline__ int cta_of(long long R, int N, long long x) {
-  return static_cast<int>(((x + 1) * N - 1) / R);
+// R slots cut into N ranges of q or q + 1: the first slot of range c, and the range of a slot.
+struct Cuts {
+  long long q;
+  int N, rem;
+};
+__device__ __forceinline__ Cuts cuts_of(long long R, int N) {
+  Cuts c;
+  c.N = N;
+  c.q = div_of(R, N);
+  c.rem = static_cast<int>(R - c.q * N);
+  return c;
+}
+__device__ __forceinline__ long long range_of(const Cuts& c, int i) { return c.q * i + min(i, c.rem); }
+__device__ __forceinline__ int cta_of(const Cuts& c, long long x) {
+  const long long wide = (c.q + 1) * c.rem;
+  return static_cast<int>(x < wide ? div_of(x, c.q + 1) : c.rem + div_of(x - wide, c.q));
 }
 
 template <int D>
@@ -242,12 +275,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
   float4* sm_acc = reinterpret_cast<float4*>(smem + S::RING);
   float* sm_m = reinterpret_cast<float*>(smem + S::ML);
   float* sm_l = sm_m + kWarps * 8;
-  float* sm_fm = reinterpret_cast<float*>(smem + S::FIN);       // [8] reference, then
-  float* sm_fl = sm_fm + 8;                                     // [8] sum of the merged row
+  float* sm_fl = reinterpret_cast<float*>(smem + S::FIN);       // [8] 1 / sum of the merged row
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::BAR);
   long long* sm_total = reinterpret_cast<long long*>(smem + S::MISC);        // [0] R, [1] first slot of the range, counted from the start of *sm_start
   int* sm_start = reinterpret_cast<int*>(smem + S::MISC + 16);               // b of the start
   int* sm_ticket = sm_start + 1;
+  int* sm_ranges = sm_start + 2;                                             // N
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   if (tid < kStages) mbar_init(full + tid, 1);
@@ -259,49 +292,82 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
   const int G = a.Hq / a.Hkv;
 
   // ---- slots of all rows, and where this CTA's range starts -------------
-  // Thread t owns `per` consecutive sequences; a block scan of their slots.
-  const int per = (a.B + kThreads - 1) / kThreads;
+  // Thread t owns `per` consecutive sequences; one block scan of their slots and
+  // (upper bits) of how many have any, and the longest row.
+  const int per = a.B <= kThreads ? 1 : (a.B + kThreads - 1) / kThreads;
   const int bt0 = tid * per, bt1 = min(bt0 + per, a.B);
+  constexpr int kCountBit = 46;           // 2^16 rows of 2^27 pairs stay below it
   long long mine = 0;
-  for (int b = bt0; b < bt1; ++b) mine += slots_of(live_of(a, b, fa));
-  mine *= a.Hkv;
+  uint32_t longest = 0;
+  for (int b = bt0; b < bt1; ++b) {
+    const uint32_t pairs = live_of(a, b, fa).pairs;
+    if (pairs) mine += (1LL << kCountBit) + static_cast<long long>(pairs + kRowCost) * a.Hkv;
+    longest = max(longest, pairs);
+  }
   long long incl = mine;
 #pragma unroll
   for (int s = 1; s < 32; s <<= 1) {
     const long long x = __shfl_up_sync(0xffffffffu, incl, s);
     if (lane >= s) incl += x;
   }
-  long long* wsum = reinterpret_cast<long long*>(sm_acc);        // [kWarps]
-  if (lane == 31) wsum[warp] = incl;
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  long long* wsum = reinterpret_cast<long long*>(sm_acc);        // [kWarps], and the longest
+  uint32_t* wmax = reinterpret_cast<uint32_t*>(wsum + kWarps);
+  if (lane == 31) {
+    wsum[warp] = incl;
+    wmax[warp] = longest;
+  }
   __syncthreads();
-  long long before = incl - mine, R = 0;
+  long long before = incl - mine, all = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     const long long x = wsum[w];
     if (w < warp) before += x;
-    R += x;
+    all += x;
+    longest = max(longest, wmax[w]);
   }
-  const int N = ranges_of(R);
-  const int cta = blockIdx.x;
+  constexpr long long kSlotMask = (1LL << kCountBit) - 1;
+  const int grid = gridDim.x, cta = blockIdx.x;
+  const long long rows = (all >> kCountBit) * a.Hkv;
+  Plan plan = {0u};
+  long long R = all & kSlotMask, at0 = before & kSlotMask, n0 = mine & kSlotMask;
+  int N = static_cast<int>(min(static_cast<long long>(grid), (R + kWarps - 1) / kWarps));
+  if (rows > 0 && rows <= grid) {
+    // Every row in k equal parts, if the longest of them is no longer than an
+    // equal share of everything and a row's cost: then no CTA has two rows to
+    // merge (an SA layer, a batch of equal lengths).
+    const uint32_t k = static_cast<uint32_t>(grid) / static_cast<uint32_t>(rows);
+    const uint32_t part = max((longest + k - 1) / k, static_cast<uint32_t>(kWarps));
+    if (static_cast<long long>(part) * grid <= R + static_cast<long long>(kRowCost) * grid) {
+      const uint32_t parts = (longest + part - 1) / part;
+      plan.even = part * parts;
+      R = rows * plan.even;
+      N = static_cast<int>(rows * parts);
+      at0 = (before >> kCountBit) * a.Hkv * plan.even;
+      n0 = (mine >> kCountBit) * a.Hkv * plan.even;
+    }
+  }
   const bool works = cta < N;
-  const long long R0 = works ? range_of(R, N, cta) : 0, R1 = works ? range_of(R, N, cta + 1) : 0;
-  if (works && R0 >= before && R0 < before + mine) {             // one thread
-    long long at = before;
+  Cuts cuts = {};
+  if (N > 0) cuts = cuts_of(R, N);
+  const long long R0 = works ? range_of(cuts, cta) : 0, R1 = works ? range_of(cuts, cta + 1) : 0;
+  if (works && R0 >= at0 && R0 < at0 + n0) {                     // one thread
+    long long at = at0;
     int b = bt0;
     for (;; ++b) {
-      const long long n = static_cast<long long>(slots_of(live_of(a, b, fa))) * a.Hkv;
+      const long long n = static_cast<long long>(slots_of(plan, live_of(a, b, fa).pairs)) * a.Hkv;
       if (R0 < at + n) break;
       at += n;
     }
     *sm_start = b;
     sm_total[0] = R;
+    *sm_ranges = N;
     sm_total[1] = R0 - at;
   }
   __syncthreads();
 
   const int g = lane >> 2, t = lane & 3;
 
-  const Unpack um = unpack_masks();
   const float sl2 = a.scale * 1.4426950408889634f;
   // The position in the range: row w, of which `done` slots are behind us, at
   // slot `pos` of the CTA's `len`.
@@ -310,9 +376,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
   const uint32_t len = static_cast<uint32_t>(R1 - R0);
   if (works) {
     w.b = *sm_start;
-    w.slots = slots_of(live_of(a, w.b, fa));
-    w.g = static_cast<int>(sm_total[1] / w.slots);
-    done = static_cast<uint32_t>(sm_total[1] % w.slots);
+    w.pairs = live_of(a, w.b, fa).pairs;
+    w.slots = slots_of(plan, w.pairs);
+    const long long off = sm_total[1];
+    w.g = static_cast<int>(div_of(off, w.slots));
+    done = static_cast<uint32_t>(off - static_cast<long long>(w.g) * w.slots);
   }
   // ---- the warp's stream of slots ---------------------------------------------
   // Slot n of the warp is number warp + kWarps n of the CTA's range and goes
@@ -320,6 +388,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
   uint8_t* ring = smem + warp * kDepth * 2 * L::BYTES;
   uint64_t* bars = full + warp * kDepth;
   const uint32_t total = (len + kWarps - 1 - warp) / kWarps;
+  // Row, done and pos stand in shared memory too: the loop over pairs, which is
+  // short of registers, wants them only at every 16th.
+  volatile uint32_t* where = reinterpret_cast<uint32_t*>(smem + S::WHERE) + warp * 8;
+  auto keep = [&]() {
+    if (lane == 0) where[0] = w.b, where[1] = w.g, where[2] = w.slots, where[3] = done, where[4] = pos, where[5] = w.pairs;
+    __syncwarp();
+  };
+  auto recall = [&]() { w.b = where[0], w.g = where[1], w.slots = where[2], done = where[3], pos = where[4], w.pairs = where[5]; };
+  keep();
   uint32_t taken = 0;          // slots consumed
   uint32_t src = kNoRecord;    // lane's record of the current 16 pairs (index into the pool), or none
   uint32_t joined = 0;         // bit 2 i: the records of the i-th of them stand side by side
@@ -330,11 +407,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
       src = kNoRecord;
       const uint32_t nl = n + (lane >> 1);
       if (nl < total) {
-        uint32_t x = done + (warp + kWarps * nl - pos);          // counted from the row's start
-        Row t = w;
+        uint32_t x = where[3] + (warp + kWarps * nl - where[4]);   // counted from the row's start
+        Row t;
+        t.b = where[0], t.g = where[1], t.slots = where[2];
         while (x >= t.slots) {
           x -= t.slots;
-          next_row(a, fa, t);
+          next_row(a, fa, plan, t);
         }
         const int k = 2 * static_cast<int>(x) + (lane & 1);
         const Live v = live_of(a, t.b, fa);
@@ -356,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
     const uint32_t i0 = __shfl_sync(0xffffffffu, src, i);
     uint8_t* dst = ring + stage * 2 * L::BYTES;
     if (joined >> i & 1u) {
-      if (lane == 0) {
+      if (elect_one()) {
         mbar_arrive_expect_tx(bars + stage, 2 * L::BYTES);
         bulk_load(dst, a.pool + static_cast<size_t>(i0) * L::BYTES, 2 * L::BYTES, bars + stage);
       }
@@ -390,18 +468,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
   }
 
   while (pos < len) {
-    const uint32_t pairs = w.slots - kRowCost;
+    float o[NT][4];
+    float l0 = 0.f, l1 = 0.f;
+    float m0 = kLowest, m1 = kLowest;          // softmax references (log2 units) of heads 2 t, 2 t + 1
+    {
     const uint32_t until = min(w.slots, done + (len - pos));       // of the row, in this range
     const uint32_t head0 = static_cast<uint32_t>(w.b) * a.Hq + w.g * G;   // the group's first query head
 
     // Query operands: lane 4 g + t holds head g, channels 32 i + 8 t + e.  And
-    // -24 times the head's group sums, cut into three bf16 numbers, as the
+    // -8 times the head's group sums, cut into three bf16 numbers, as the
     // second operand of an MMA whose first is the tokens' scales: row 2 t + e
     // of that product is (at d 128) piece t / 2 of group 2 (t % 2) + e, rows 8
     // and up the last piece; at d 64 piece t of group e.
     uint32_t qf[GR][4], bq0 = 0, bq1 = 0;
+    float sc0, sc1;            // log2 units per unit of a score, of heads 2 t and 2 t + 1
     {
       float c[GR];
+      uint32_t top = 0;
 #pragma unroll
       for (int i = 0; i < GR; ++i) {
         uint4 v = {0, 0, 0, 0};
@@ -410,13 +493,32 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
         qf[i][1] = v.y;
         qf[i][2] = v.z;
         qf[i][3] = v.w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = max(top, max(qf[i][e] << 16 & 0x7fffffffu, qf[i][e] & 0x7fff0000u));
+      }
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // The head times 2^k, its largest channel then next to 2^126; the odd pairs
+      // 2^4 less.  Scores come out times 2^(k - 133).
+      const int k = min(126, max(6, 126 + 127 - static_cast<int>(top >> 23)));
+      const float up = __uint_as_float((127 + k) << 23), less = __uint_as_float((127 + k - 4) << 23);
+      const float down = __uint_as_float(max(1, 127 + k - 130) << 23);
+#pragma unroll
+      for (int i = 0; i < GR; ++i) {
         float sum = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sum += bf16lo_to_f32(qf[i][e]) + bf16hi_to_f32(qf[i][e]);
+        for (int e = 0; e < 4; ++e) {
+          const float lo = bf16lo_to_f32(qf[i][e]), hi = bf16hi_to_f32(qf[i][e]);
+          sum += lo * down + hi * down;
+          qf[i][e] = e & 1 ? pack_bf16x2(lo * less, hi * less) : pack_bf16x2(lo * up, hi * up);
+        }
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        c[i] = -24.f * sum;
+        c[i] = -sum;
       }
+      const float back = sl2 * __uint_as_float((127 + 133 - k) << 23);
+      sc0 = __shfl_sync(0xffffffffu, back, 8 * t);
+      sc1 = __shfl_sync(0xffffffffu, back, 8 * t + 4);
       float e0 = c[0], e1 = c[1];
       if constexpr (D == 128) {
         if (t & 1) {
@@ -443,11 +545,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
     if (pos + (until - done) < len && lane < G * D / 64 && head0 + 2 * G <= static_cast<uint32_t>(a.B) * a.Hq)
       asm volatile("prefetch.global.L1 [%0];" ::"l"(a.q + static_cast<size_t>(head0 + G) * D + lane * 64));
 
-    float o[NT][4];
 #pragma unroll
     for (int m = 0; m < NT; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
-    float l0 = 0.f, l1 = 0.f;
-    float m0 = kLowest, m1 = kLowest;          // softmax references (log2 units) of heads 2 t, 2 t + 1
     float th0 = kLowest, th1 = kLowest;        // a score (before the scale) above it moves the reference
 
     // The warp takes every kWarps-th slot of the CTA's range.
@@ -459,7 +558,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
       plain2 = v.plain2;
       plain3 = v.plain3;
     }
-    for (int j = static_cast<int>(done + skip); j < static_cast<int>(until) && ok; j += kWarps, ++taken) {
+    const int j_end = static_cast<int>(until);
+    for (int j = static_cast<int>(done + skip); j < j_end && ok; j += kWarps, ++taken) {
       const uint32_t stage = taken & (kDepth - 1), parity = (taken / kDepth) & 1u;
       const uint32_t none = missing & 3u;
       missing >>= 2;
@@ -508,14 +608,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
 #pragma unroll
         for (int i = 0; i < GR; ++i) {
           float acc[4];
+          const uint32_t y0 = __funnelshift_r(k0[i], k0[i], 3), y1 = __funnelshift_r(k1[i], k1[i], 3);
           {
-            const uint32_t af[4] = {k_pair<0>(k0[i], um), k_pair<0>(k1[i], um), k_pair<1>(k0[i], um),
-                                    k_pair<1>(k1[i], um)};
+            const uint32_t af[4] = {fields<0>(y0), fields<0>(y1), fields<1>(y0), fields<1>(y1)};
             mma_zero(acc, af, qf[i][0], qf[i][1]);
           }
           {
-            const uint32_t af[4] = {k_pair<2>(k0[i], um), k_pair<2>(k1[i], um), k_pair<3>(k0[i], um),
-                                    k_pair<3>(k1[i], um)};
+            const uint32_t z0 = y0 >> 8, z1 = y1 >> 8;
+            const uint32_t af[4] = {fields<2>(z0), fields<2>(z1), fields<3>(z0), fields<3>(z1)};
             mma_add(acc, af, qf[i][2], qf[i][3]);
           }
           x[r][0] = fmaf(s0[i], acc[0], x[r][0]);
@@ -545,22 +645,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
           if (!live(u0 + 2 * t + 9)) sv1[r] &= 0x0000ffffu;
         }
       }
+      bool large = (((sv0[0] + kLarge) | (sv1[0] + kLarge) | (sv0[1] + kLarge) | (sv1[1] + kLarge)) & 0x80008000u) != 0;
       const float t0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
       const float t1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
-      if (__any_sync(0xffffffffu, t0 > th0 || t1 > th1)) {
+      if (__any_sync(0xffffffffu, t0 > th0 || t1 > th1 || large)) {
+        large = __any_sync(0xffffffffu, large);
         float n0 = t0, n1 = t1;
 #pragma unroll
         for (int s = 4; s < 32; s <<= 1) {
           n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, s));
           n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, s));
         }
-        n0 = fmaxf(m0, n0 * sl2);
-        n1 = fmaxf(m1, n1 * sl2);
+        n0 = fmaxf(m0, n0 * sc0);
+        n1 = fmaxf(m1, n1 * sc1);
         const float f0 = ex2(m0 - n0), f1 = ex2(m1 - n1);
         m0 = n0;
         m1 = n1;
-        th0 = (n0 + kGrow) / sl2;
-        th1 = (n1 + kGrow) / sl2;
+        th0 = (n0 + kGrow) / sc0;
+        th1 = (n1 + kGrow) / sc1;
         l0 *= f0;
         l1 *= f1;
 #pragma unroll
@@ -573,38 +675,67 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
       }
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float p00 = ex2(fmaf(x[r][0], sl2, -m0)), p01 = ex2(fmaf(x[r][1], sl2, -m1));
-        const float p10 = ex2(fmaf(x[r][2], sl2, -m0)), p11 = ex2(fmaf(x[r][3], sl2, -m1));
+        const float p00 = ex2(fmaf(x[r][0], sc0, -m0)), p01 = ex2(fmaf(x[r][1], sc1, -m1));
+        const float p10 = ex2(fmaf(x[r][2], sc0, -m0)), p11 = ex2(fmaf(x[r][3], sc1, -m1));
         l0 += p00 + p10;
         l1 += p01 + p11;
-        const uint32_t b0 = movmatrix_trans(pack_bf16x2(p00, p01));
-        const uint32_t b1 = movmatrix_trans(pack_bf16x2(p10, p11));
-        // -24 s (exact: 5 bits times 3)
-        const uint32_t n0 = fma_bf16x2(sv0[r], 0xc1c0c1c0u, 0u), n1 = fma_bf16x2(sv1[r], 0xc1c0c1c0u, 0u);
+        if (!large) {
+          const uint32_t b0 = movmatrix_trans(pack_bf16x2(p00, p01));
+          const uint32_t b1 = movmatrix_trans(pack_bf16x2(p10, p11));
+          const uint32_t e0 = mul_bf16x2(sv0[r], kUpEven), e1 = mul_bf16x2(sv1[r], kUpEven);
+          const uint32_t o0 = mul_bf16x2(sv0[r], kUpOdd), o1 = mul_bf16x2(sv1[r], kUpOdd);
+          const uint32_t n0 = mul_bf16x2(sv0[r], kDown8), n1 = mul_bf16x2(sv1[r], kDown8);
 #pragma unroll
-        for (int i = 0; i < GR; ++i) {
-          const uint32_t a0 = v0[r][i], a1 = v1[r][i];
-          {
-            const uint32_t af[4] = {
-                fma_bf16x2(v_pair<0>(a0, um), sv0[r], n0), fma_bf16x2(v_pair<1>(a0, um), sv0[r], n0),
-                fma_bf16x2(v_pair<0>(a1, um), sv1[r], n1), fma_bf16x2(v_pair<1>(a1, um), sv1[r], n1)};
-            mma_add(o[2 * i], af, b0, b1);
+          for (int i = 0; i < GR; ++i) {
+            const uint32_t y0 = v0[r][i], y1 = v1[r][i], z0 = y0 >> 8, z1 = y1 >> 8;
+            {
+              const uint32_t af[4] = {fma_bf16x2(fields<0>(y0), e0, n0), fma_bf16x2(fields<1>(y0), o0, n0),
+                                      fma_bf16x2(fields<0>(y1), e1, n1), fma_bf16x2(fields<1>(y1), o1, n1)};
+              mma_add(o[2 * i], af, b0, b1);
+            }
+            {
+              const uint32_t af[4] = {fma_bf16x2(fields<2>(z0), e0, n0), fma_bf16x2(fields<3>(z0), o0, n0),
+                                      fma_bf16x2(fields<2>(z1), e1, n1), fma_bf16x2(fields<3>(z1), o1, n1)};
+              mma_add(o[2 * i + 1], af, b0, b1);
+            }
           }
-          {
-            const uint32_t af[4] = {
-                fma_bf16x2(v_pair<2>(a0, um), sv0[r], n0), fma_bf16x2(v_pair<3>(a0, um), sv0[r], n0),
-                fma_bf16x2(v_pair<2>(a1, um), sv1[r], n1), fma_bf16x2(v_pair<3>(a1, um), sv1[r], n1)};
-            mma_add(o[2 * i + 1], af, b0, b1);
+        } else {
+          // Large values: 16 + u from the mantissa, (16 + u) scale - 24 scale the
+          // value itself, and 2^-25 on the other operand.
+          const float f = 1.f / kValueUnit;
+          const uint32_t b0 = movmatrix_trans(pack_bf16x2(p00 * f, p01 * f));
+          const uint32_t b1 = movmatrix_trans(pack_bf16x2(p10 * f, p11 * f));
+          const uint32_t n0 = mul_bf16x2(sv0[r], 0xc1c0c1c0u), n1 = mul_bf16x2(sv1[r], 0xc1c0c1c0u);   // -24
+          auto value = [](uint32_t x, uint32_t scale, uint32_t n) {
+            return fma_bf16x2((x & 0x00780078u) | 0x41804180u, scale, n);
+          };
+#pragma unroll
+          for (int i = 0; i < GR; ++i) {
+            const uint32_t y0 = v0[r][i], y1 = v1[r][i];
+            {
+              const uint32_t af[4] = {value(y0 << 3, sv0[r], n0), value(y0 >> 1, sv0[r], n0),
+                                      value(y1 << 3, sv1[r], n1), value(y1 >> 1, sv1[r], n1)};
+              mma_add(o[2 * i], af, b0, b1);
+            }
+            {
+              const uint32_t af[4] = {value(y0 >> 5, sv0[r], n0), value(y0 >> 9, sv0[r], n0),
+                                      value(y1 >> 5, sv1[r], n1), value(y1 >> 9, sv1[r], n1)};
+              mma_add(o[2 * i + 1], af, b0, b1);
+            }
           }
         }
       }
     }
-
+    }
+    recall();
+    const uint32_t pairs = w.pairs, until = min(w.slots, done + (len - pos));
+    const uint32_t head0 = static_cast<uint32_t>(w.b) * a.Hq + w.g * G;
     const bool begins = done == 0, ends = until >= pairs;
     if (done >= pairs) {       // the range began in the row's empty slots
       pos += until - done;
       done = 0;
-      if (pos < len) next_row(a, fa, w);
+      if (pos < len) next_row(a, fa, plan, w);
+      keep();
       continue;
     }
     // ---- merge the warps --------------------------------------------------
@@ -655,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
         r = make_float4(0.f, 0.f, 0.f, 0.f);
       }
       if (whole) {
-        const float i0 = ls0 != 0.f ? 1.f / ls0 : 0.f, i1 = ls1 != 0.f ? 1.f / ls1 : 0.f;
+        const float i0 = ls0 != 0.f ? kValueUnit / ls0 : 0.f, i1 = ls1 != 0.f ? kValueUnit / ls1 : 0.f;
         uint16_t* out = a.o + static_cast<size_t>(head0 + h) * D + gi * (D / 8) + 2 * m;
         *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(r.x * i0, r.z * i0);
         if (h + 1 < G) *reinterpret_cast<uint32_t*>(out + D) = pack_bf16x2(r.y * i1, r.w * i1);
@@ -675,13 +806,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
     }
     if (!whole) {
       // ---- merge the CTAs of a row: the one that comes last ----------------
-      const long long Rt = sm_total[0];
-      const int Nt = ranges_of(Rt);
-      const long long row0 = range_of(Rt, Nt, cta) + pos - done;
-      const int first = cta_of(Rt, Nt, row0), last = cta_of(Rt, Nt, row0 + pairs - 1);
-      __threadfence();
+      const Cuts c = cuts_of(sm_total[0], *sm_ranges);
+      const long long row0 = range_of(c, cta) + pos - done;
+      const int first = cta_of(c, row0), last = cta_of(c, row0 + pairs - 1);
       named_bar_sync(1, kThreads);
       if (tid == 0) {
+        // the barrier orders the CTA's stores before this, the fence before the ticket
+        __threadfence();
         int* ticket = a.tickets + static_cast<size_t>(w.b) * a.Hkv + w.g;
         const int n = atomicAdd(ticket, 1);
         *sm_ticket = n;
@@ -695,34 +826,31 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
         const int f0 = 2 * first + 1;
         float* wt = reinterpret_cast<float*>(sm_acc);              // [part][8] weights
         const int np = last - first + 1;
-        for (int i = tid; i < 8 * np; i += kThreads) {
-          const int c = i >> 3, h = i & 7;
-          const int sl = c == 0 ? f0 : 2 * (first + c);
-          wt[i] = h < G ? __ldcg(part_m + sl * 8 + h) : kLowest;
-        }
-        named_bar_sync(1, kThreads);
-        if (tid < 8) {
-          float M = kLowest;
-          for (int c = 0; c < np; ++c) M = fmaxf(M, wt[c * 8 + tid]);
-          sm_fm[tid] = M;
-        }
-        named_bar_sync(1, kThreads);
-        for (int i = tid; i < 8 * np; i += kThreads) {
-          wt[i] = ex2(wt[i] - sm_fm[i & 7]);
-        }
-        named_bar_sync(1, kThreads);
-        if (tid < 8 && tid < G) {
-          float ls = 0.f;
+        // Warp h: the weights of head h's parts, and the row's sum.
+        if (warp < G) {
+          float M = kLowest, ls = 0.f;
           bool lost = false;
-          for (int c = 0; c < np; ++c) {
-            const float l = __ldcg(part_l + (c == 0 ? f0 : 2 * (first + c)) * 8 + tid);
-            lost |= l < 0.f;
-            ls = fmaf(wt[c * 8 + tid], l, ls);
+          for (int c = lane; c < np; c += 32) {
+            const float m = __ldcg(part_m + (c == 0 ? f0 : 2 * (first + c)) * 8 + warp);
+            wt[c * 8 + warp] = m;
+            M = fmaxf(M, m);
           }
-          if (lost) ls = 0.f;
-          sm_fl[tid] = ls != 0.f ? 1.f / ls : 0.f;
-          if (a.lse)
-            a.lse[head0 + tid] = ls != 0.f ? (sm_fm[tid] + log2f(ls)) * 0.69314718055994531f : -INFINITY;
+#pragma unroll
+          for (int s = 1; s < 32; s <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+          for (int c = lane; c < np; c += 32) {
+            const float l = __ldcg(part_l + (c == 0 ? f0 : 2 * (first + c)) * 8 + warp);
+            const float e = ex2(wt[c * 8 + warp] - M);
+            wt[c * 8 + warp] = e;
+            lost |= l < 0.f;
+            ls = fmaf(e, l, ls);
+          }
+#pragma unroll
+          for (int s = 1; s < 32; s <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, s);
+          if (__any_sync(0xffffffffu, lost)) ls = 0.f;
+          if (lane == 0) {
+            sm_fl[warp] = ls != 0.f ? kValueUnit / ls : 0.f;
+            if (a.lse) a.lse[head0 + warp] = ls != 0.f ? (M + log2f(ls)) * 0.69314718055994531f : -INFINITY;
+          }
         }
         named_bar_sync(1, kThreads);
         for (int i = tid; i < S::PART4; i += kThreads) {
@@ -732,13 +860,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
 #pragma unroll 8
           for (int c = 0; c < np; ++c) {
             const float4 v = __ldcg(part + static_cast<size_t>(c == 0 ? f0 : 2 * (first + c)) * S::PART4 + i);
-            const float w0 = wt[c * 8 + h], w1 = wt[c * 8 + h + 1];
+            const float w0 = wt[c * 8 + h], w1 = h + 1 < G ? wt[c * 8 + h + 1] : 0.f;
             r.x = fmaf(w0, v.x, r.x);
             r.y = fmaf(w1, v.y, r.y);
             r.z = fmaf(w0, v.z, r.z);
             r.w = fmaf(w1, v.w, r.w);
           }
-          const float i0 = sm_fl[h], i1 = sm_fl[h + 1];
+          const float i0 = sm_fl[h], i1 = h + 1 < G ? sm_fl[h + 1] : 0.f;
           uint16_t* out = a.o + static_cast<size_t>(head0 + h) * D + gi * (D / 8) + 2 * m;
           *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(r.x * i0, r.z * i0);
           if (h + 1 < G) *reinterpret_cast<uint32_t*>(out + D) = pack_bf16x2(r.y * i1, r.w * i1);
@@ -748,7 +876,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
     pos += until - done;
     done = 0;
     if (pos < len) {
-      next_row(a, fa, w);
+      next_row(a, fa, plan, w);
+      keep();
       named_bar_sync(1, kThreads);      // the merge buffer is free again
     }
   }

@@ -27,7 +27,7 @@ class Cache:
     """Requests of given lengths in a cache whose free bytes are 0xFF (NaN scales) and whose
     table holds nonsense behind each request's pages."""
 
-    def __init__(self, ctx, lens, Hkv, d, page, seed=0, std=1.0, width=None):
+    def __init__(self, ctx, lens, Hkv, d, page, seed=0, std=1.0, width=None, vstd=1.0, edit=None):
         self.lens, self.Hkv, self.d, self.page = lens, Hkv, d, page
         need = [-(-n // page) for n in lens]
         pages = sum(need) + 3
@@ -41,7 +41,9 @@ class Cache:
         self.table = torch.tensor(table, dtype=torch.int32, device="cuda")
         self.sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
         self.k = [normal((n, Hkv, d), seed + 10 + b, std) for b, n in enumerate(lens)]
-        self.v = [normal((n, Hkv, d), seed + 500 + b) for b, n in enumerate(lens)]
+        self.v = [normal((n, Hkv, d), seed + 500 + b, vstd) for b, n in enumerate(lens)]
+        if edit:
+            edit(self)
         for b, n in enumerate(lens):
             if n:
                 u = torch.arange(n, device="cuda")
@@ -155,6 +157,38 @@ def test_sharp_and_flat_scores(ctx, std, scale):
     q = normal((2, 8, 128), 7)
     o, lse = c.decode(ctx, q, scale=scale)
     c.check(q, o, lse, scale=scale)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("qstd,kstd,vstd", [(1e-30, 1.0, 1.0), (1e30, 1e-30, 1.0), (1e-30, 1e30, 1.0),
+                                            (1.0, 1.0, 1e-25), (1.0, 1.0, 3e6), (1.0, 1.0, 1e25),
+                                            (1e10, 1e-20, 1e12), (0.0, 1.0, 1.0)])
+def test_magnitudes(ctx, d, qstd, kstd, vstd):
+    """Queries, keys and values far from 1: the largest and smallest that the 4-bit form holds
+    well within, values around the size at which the kernel changes its arithmetic."""
+    c = Cache(ctx, [700, 45], 2, d, 32, seed=20, std=kstd, vstd=vstd)
+    q = normal((2, 8, d), 21, qstd)
+    o, lse = c.decode(ctx, q)
+    ctx.check()
+    c.check(q, o, lse)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_few_large_values_and_channels(ctx, d):
+    """Single tokens of 1e9 among values of 1, one channel of the query 1e6 times the others
+    and one of the keys, a head of the query zero."""
+    def edit(c):
+        c.v[0][::37] *= 1e9
+        c.v[0][5, 0, 32:64] = 0
+        c.k[0][..., 7] *= 1e6
+        c.k[1][..., 40] *= 1e-6
+    c = Cache(ctx, [900, 33], 2, d, 16, seed=22, edit=edit)
+    q = normal((2, 8, d), 23)
+    q[..., 7] *= 1e-6
+    q[:, 1, 40] *= 1e6
+    q[1, 3] = 0
+    o, lse = c.decode(ctx, q)
+    c.check(q, o, lse)
 
 
 def test_nan_stays_with_its_request_and_head(ctx):
