@@ -192,6 +192,19 @@ def test_cache_beyond_32_bits(ctx):
     assert same_values(ko, k) and same_values(vo, v)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_read_into_rows_that_start_at_16_bytes(ctx, d):
+    N, Hkv, page = 700, 8, 32
+    pool = pool_of(24, Hkv, page, d)
+    k, v = normal((N, Hkv, d), 17), normal((N, Hkv, d), 18)
+    slots = run_slots(N, page, 5, 24)
+    ctx.kv_write_q4(k, v, slots, pool)
+    out = [torch.zeros(N * Hkv * d + 8, dtype=torch.bfloat16, device="cuda")[8:].view(N, Hkv, d) for _ in range(2)]
+    assert out[0].data_ptr() % 32 == 16
+    ctx.kv_read_q4(pool, slots, *out)
+    assert same_values(out[0], k) and same_values(out[1], v)
+
+
 def test_refusals(ctx):
     pool = pool_of(3, 2, 16, 64)
     k = normal((4, 2, 64), 1)
