@@ -62,7 +62,7 @@ __device__ __forceinline__ Quant quantise8(const uint4& x) {
   // top / 7 by a product with a little more than 1 / 7 (by 2^-20 of it): top has 8
   // significant bits, so top / 7 is a 5-bit number exactly, which the product
   // passes by less than the cut takes off, or at least 2^-9 of itself below the next.
-  uint32_t sbits = __float_as_uint(__uint_as_float(top) * 0x1.24925b6db6db7p-3f) & 0xfff80000u;
+  uint32_t sbits = __float_as_uint(__uint_as_float(top) * 0x1.24925cp-3f) & 0xfff80000u;
   Quant out;
   out.plain = top >= kQ4LowBits && top <= kQ4HighBits;
   if (top < kQ4LowBits) sbits = 0;

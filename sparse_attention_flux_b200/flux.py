@@ -533,7 +533,7 @@ class Context:
                 raise ValueError("norm weights must have head_dim entries")
         _check(lib().flux_qk_norm_rope(
             self._h, q_at, q_stride, k_at, k_stride, qo_at, qo_stride, ko_at, ko_stride, N, Hq,
-            Hkv, d, qw_at, kw_at, eps, pos_at, freq_at, 2 * inv_freq.numel(),
+            Hkv, d, qw_at, kw_at, float(eps), pos_at, freq_at, 2 * inv_freq.numel(),
             1 if interleaved else 0, self._on(stream)))
 
     def kv_write_q4(self, k_src, v_src, slots, kv_pool, stream=None):
@@ -586,7 +586,7 @@ class Context:
         _check(lib().flux_attn_decode_q4(self._h, q_at, pool_at, num_pages, page_size, table_at,
                                          table[1], lens_at, o_at, lse_at, B, Hq,
                                          kv_pool.shape[1], d, mode_at, layer, sink_blocks,
-                                         window_blocks, block, scale, self._on(stream)))
+                                         window_blocks, block, float(scale), self._on(stream)))
 
 
 def attn_decode_noalloc(q, k_cache, v_cache, seqlens, o, scale: float, layer_mode=None,
