@@ -330,6 +330,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
   const int grid = gridDim.x, cta = blockIdx.x;
   const long long rows = (all >> kCountBit) * a.Hkv;
   Plan plan = {0u};
+  Cuts cuts = {};
   long long R = all & kSlotMask, at0 = before & kSlotMask, n0 = mine & kSlotMask;
   int N = static_cast<int>(min(static_cast<long long>(grid), (R + kWarps - 1) / kWarps));
   if (rows > 0 && rows <= grid) {
@@ -345,11 +346,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
       N = static_cast<int>(rows * parts);
       at0 = (before >> kCountBit) * a.Hkv * plan.even;
       n0 = (mine >> kCountBit) * a.Hkv * plan.even;
+      cuts.q = part;
     }
   }
-  const bool works = cta < N;
-  Cuts cuts = {};
-  if (N > 0) cuts = cuts_of(R, N);
+  const bool works = cta < N, empties = (all >> kCountBit) != a.B;
+  if (N > 0 && !plan.even) cuts = cuts_of(R, N);
+  cuts.N = N;
   const long long R0 = works ? range_of(cuts, cta) : 0, R1 = works ? range_of(cuts, cta + 1) : 0;
   if (works && R0 >= at0 && R0 < at0 + n0) {                     // one thread
     long long at = at0;
@@ -454,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
   for (uint32_t n = 0; n < kDepth && n < total; ++n) fill(n, n);
 
   // Sequences with no live token: zero output, lse -inf.
-  for (int b = cta; b < a.B; b += gridDim.x) {
+  for (int b = empties ? cta : a.B; b < a.B; b += gridDim.x) {
     if (live_of(a, b, fa).pairs != 0) continue;
     if (tid == 0) {
       const int s = a.seqlens[b];
@@ -811,17 +813,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
       const int first = cta_of(c, row0), last = cta_of(c, row0 + pairs - 1);
       named_bar_sync(1, kThreads);
       if (tid == 0) {
-        // the barrier orders the CTA's stores before this, the fence before the ticket
-        __threadfence();
+        // The barrier orders the CTA's stores before the ticket, which releases them
+        // and acquires those of the CTAs before; the next barrier passes that on.
         int* ticket = a.tickets + static_cast<size_t>(w.b) * a.Hkv + w.g;
-        const int n = atomicAdd(ticket, 1);
+        int n;
+        asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(n) : "l"(ticket) : "memory");
         *sm_ticket = n;
         if (n == last - first) *ticket = 0;
-        __threadfence();
       }
       named_bar_sync(1, kThreads);
       if (*sm_ticket == last - first) {
-        __threadfence();
         // slot of part c: the first CTA's row begins there, the others' before
         const int f0 = 2 * first + 1;
         float* wt = reinterpret_cast<float*>(sm_acc);              // [part][8] weights
