@@ -827,24 +827,34 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
         const int f0 = 2 * first + 1;
         float* wt = reinterpret_cast<float*>(sm_acc);              // [part][8] weights
         const int np = last - first + 1;
-        // Warp h: the weights of head h's parts, and the row's sum.
+        // A thread's float4 of the first parts, while the weights are worked out.
+        const int i = tid, h = 2 * (i & 3), gi = (i & 31) >> 2, m = i >> 5;
+        const bool act = i < S::PART4 && h < G;
+        static_assert(S::PART4 <= kThreads, "one float4 per thread");
+        auto part_of = [&](int c) { return part + static_cast<size_t>(c == 0 ? f0 : 2 * (first + c)) * S::PART4 + i; };
+        constexpr int kAhead = 8;
+        float4 ahead[kAhead];
+#pragma unroll
+        for (int c = 0; c < kAhead; ++c)
+          ahead[c] = act && c < np ? __ldcg(part_of(c)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        // Warp v: the weights of head v's parts, and the row's sum.
         if (warp < G) {
           float M = kLowest, ls = 0.f;
           bool lost = false;
           for (int c = lane; c < np; c += 32) {
-            const float m = __ldcg(part_m + (c == 0 ? f0 : 2 * (first + c)) * 8 + warp);
-            wt[c * 8 + warp] = m;
-            M = fmaxf(M, m);
+            const int at = (c == 0 ? f0 : 2 * (first + c)) * 8 + warp;
+            const float pm = __ldcg(part_m + at), pl = __ldcg(part_l + at);
+            lost |= pl < 0.f;
+            const float M1 = fmaxf(M, pm);
+            ls = fmaf(pl, ex2(pm - M1), ls * ex2(M - M1));
+            M = M1;
+            wt[c * 8 + warp] = pm;
           }
+          const float mine = M;
 #pragma unroll
           for (int s = 1; s < 32; s <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
-          for (int c = lane; c < np; c += 32) {
-            const float l = __ldcg(part_l + (c == 0 ? f0 : 2 * (first + c)) * 8 + warp);
-            const float e = ex2(wt[c * 8 + warp] - M);
-            wt[c * 8 + warp] = e;
-            lost |= l < 0.f;
-            ls = fmaf(e, l, ls);
-          }
+          ls *= ex2(mine - M);
+          for (int c = lane; c < np; c += 32) wt[c * 8 + warp] = ex2(wt[c * 8 + warp] - M);
 #pragma unroll
           for (int s = 1; s < 32; s <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, s);
           if (__any_sync(0xffffffffu, lost)) ls = 0.f;
@@ -854,19 +864,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
           }
         }
         named_bar_sync(1, kThreads);
-        for (int i = tid; i < S::PART4; i += kThreads) {
-          const int h = 2 * (i & 3), gi = (i & 31) >> 2, m = i >> 5;
-          if (h >= G) continue;
+        if (act) {
           float4 r = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-          for (int c = 0; c < np; ++c) {
-            const float4 v = __ldcg(part + static_cast<size_t>(c == 0 ? f0 : 2 * (first + c)) * S::PART4 + i);
+          auto add = [&](int c, const float4& v) {
             const float w0 = wt[c * 8 + h], w1 = h + 1 < G ? wt[c * 8 + h + 1] : 0.f;
             r.x = fmaf(w0, v.x, r.x);
             r.y = fmaf(w1, v.y, r.y);
             r.z = fmaf(w0, v.z, r.z);
             r.w = fmaf(w1, v.w, r.w);
-          }
+          };
+#pragma unroll
+          for (int c = 0; c < kAhead; ++c)
+            if (c < np) add(c, ahead[c]);
+#pragma unroll 8
+          for (int c = kAhead; c < np; ++c) add(c, __ldcg(part_of(c)));
           const float i0 = sm_fl[h], i1 = h + 1 < G ? sm_fl[h + 1] : 0.f;
           uint16_t* out = a.o + static_cast<size_t>(head0 + h) * D + gi * (D / 8) + 2 * m;
           *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(r.x * i0, r.z * i0);
