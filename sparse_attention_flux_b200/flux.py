@@ -493,22 +493,26 @@ class Context:
         old_lens to new_lens; pages come from free_pages[cursor:].  window_pages > 0: a ring of
         sink + window pages per request (SA layers)."""
         i32 = self._i32
-        args = [_at(t, i32, n_, self) for n_, t in (
-            ("old_lens", old_lens), ("new_lens", new_lens), ("free_pages", free_pages),
-            ("cursor", cursor), ("cursor_out", cursor_out), ("page_table", page_table),
-            ("positions", positions), ("cu_new", cu_new))]
+        old_at = _at(old_lens, i32, "old_lens", self)
+        new_at = _at(new_lens, i32, "new_lens", self)
+        free_at = _at(free_pages, i32, "free_pages", self)
+        cursor_at = _at(cursor, i32, "cursor", self)
+        out_at = cursor_at if cursor_out is cursor else _at(cursor_out, i32, "cursor_out", self)
+        table_at = _at(page_table, i32, "page_table", self)
+        pos_at = _at(positions, i32, "positions", self)
+        cu_at = _at(cu_new, i32, "cu_new", self)
         slots_at = _at(slots, self._i64, "slots", self)
         B, n_slots, table = old_lens.numel(), slots.numel(), page_table.shape
         if len(table) != 2 or table[0] != B or new_lens.numel() != B:
             raise ValueError("old_lens / new_lens / page_table shapes are inconsistent")
-        if positions.numel() != n_slots or cursor.numel() < 1 or cursor_out.numel() < 1:
+        if positions.numel() != n_slots or not cursor.numel() or not cursor_out.numel():
             raise ValueError("slots / positions / cursor shapes are inconsistent")
         if cu_new is not None and cu_new.numel() < B + 1:
             raise ValueError("cu_new needs B + 1 entries")
         _check(lib().flux_build_page_table(
-            self._h, args[0], args[1], B, page_size, sink_pages, window_pages, args[2],
-            free_pages.numel(), args[3], args[4], args[5], table[1], slots_at, args[6], n_slots,
-            args[7], self._on(stream)))
+            self._h, old_at, new_at, B, page_size, sink_pages, window_pages, free_at,
+            free_pages.numel(), cursor_at, out_at, table_at, table[1], slots_at, pos_at, n_slots,
+            cu_at, self._on(stream)))
 
     def qk_norm_rope(self, q, k, q_out, k_out, positions, inv_freq, q_weight=None, k_weight=None,
                      eps: float = 1e-6, interleaved: bool = False, stream=None):
