@@ -78,7 +78,7 @@ def test_small_steps(ctx, page, old, new, sink, window):
     ctx.check()
 
 
-@pytest.mark.parametrize("B", [1, 31, 32, 1023, 1025, 3000, 8192])
+@pytest.mark.parametrize("B", [1, 31, 32, 1023, 1025, 3000, 5200, 6120, 8192])
 @pytest.mark.parametrize("window", [0, 3])
 def test_many_requests(ctx, B, window):
     g = np.random.default_rng(B)
