@@ -31,8 +31,9 @@
  *   - Every call is asynchronous on `stream` (a cudaStream_t; NULL = the
  *     legacy default stream) and returns an int status.  Host-side argument
  *     checks happen before any launch; on failure nothing is launched.
- *   - Stream order holds as usual.  The decode calls and the router's second
- *     kernel are launched with programmatic stream serialisation: their CTAs
+ *   - Stream order holds as usual.  The decode calls, the calls of the paged
+ *     4-bit cache and the router's second kernel are launched with
+ *     programmatic stream serialisation: their CTAs
  *     may be dispatched while the previous kernel on the stream finishes, but
  *     they read and write no memory until that kernel has completed and its
  *     writes are visible, so the caller sees ordinary stream semantics.
@@ -455,8 +456,8 @@ int flux_decode_workspace_bytes(flux_ctx* ctx, int B, int Hq, int Hkv, int d, in
  * tokens are read is a device-checked error and leaves those tokens out; other
  * entries are never read.  Bytes behind a sequence's last token are never
  * used, whatever they hold.  q, o, lse, layer_mode, sink / window / block,
- * scale and the group limits as flux_attn_decode.  Split partials live in the
- * ctx workspace (flux_decode_q4_workspace_bytes). */
+ * scale and the group limits as flux_attn_decode.  |q| below 2^120.  Split
+ * partials live in the ctx workspace (flux_decode_q4_workspace_bytes). */
 int flux_build_page_table(flux_ctx* ctx, const int32_t* old_lens, const int32_t* new_lens, int B,
                           int page_size, int sink_pages, int window_pages,
                           const int32_t* free_pages, int n_free, const int32_t* cursor,

@@ -18,9 +18,9 @@
 // memory as a whole record by the warp in whose window they start; the tokens
 // that are in no such run (the ends of a prompt's part of a page, requests of
 // one token) go one at a time.  Short calls take a warp per token and kv head.
-// 65536 tokens, 8 kv heads, d 128, written and read back: 124 us, 5.5 TB/s of
-// 687 MB (a warp per token 369 us; 4 CTAs per SM writing, 100 registers, 131;
-// V rows read back by 16-byte instead of 32-byte stores 138).
+// 65536 tokens, 8 kv heads, d 128, written and read back: 122 us, 5.6 TB/s of
+// 687 MB (a warp per token 369 us; 4 CTAs per SM writing, 100 registers, 131; one
+// quotient at a time 124; V rows read back by 16-byte instead of 32-byte stores 138).
 #include "q4.h"
 
 namespace flux {
@@ -46,6 +46,11 @@ __device__ __forceinline__ bool valid_slot(const KvQ4Launch& a, int64_t slot, bo
 // 8 consecutive channels of the lane, quantised; the group of 32 is the lane's
 // aligned quartet.  bits[e] = kCodeBits + code (mod 2^32).
 constexpr uint32_t kCodeBits = 0x4b400000u;      // 1.5 * 2^23: adding it to a float rounds to whole numbers
+__device__ __forceinline__ unsigned long long pack2(float lo, float hi) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
 struct Quant {
   uint32_t bits[8];
   uint32_t scale;          // bf16 bits
@@ -71,14 +76,19 @@ __device__ __forceinline__ Quant quantise8(const uint4& x) {
   const float s = __uint_as_float(sbits);
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  // f / s by a product and one residual step (Markstein), two at a time: where
+  // f / s is a float, the residual is exact and so is the result, whatever the last
+  // bits of r; else it is off by a rounding or two, and no border is that near.
+  const unsigned long long r2 = pack2(r, r), s2 = pack2(-s, -s), m2 = pack2(12582920.f, 12582920.f);   // 1.5 * 2^23 + 8
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float f = e & 1 ? bf16hi_to_f32(w[e / 2]) : bf16lo_to_f32(w[e / 2]);
-    // f / s by a product and one residual step (Markstein): where f / s is a
-    // float, the residual is exact and so is the result, whatever the last bits of
-    // r; else it is off by a rounding or two, and no border is that near.
-    const float q0 = f * r, q = fmaf(fmaf(-q0, s, f), r, q0);
-    out.bits[e] = __float_as_uint(q + 12582920.f);   // 1.5 * 2^23 + 8
+  for (int i = 0; i < 4; ++i) {
+    const unsigned long long f = pack2(bf16lo_to_f32(w[i]), bf16hi_to_f32(w[i]));
+    unsigned long long q, t;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(f), "l"(r2));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(t) : "l"(q), "l"(s2), "l"(f));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(t), "l"(r2), "l"(q));
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(q), "l"(m2));
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(out.bits[2 * i]), "=r"(out.bits[2 * i + 1]) : "l"(q));
   }
   return out;
 }
