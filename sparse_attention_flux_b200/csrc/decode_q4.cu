@@ -184,8 +184,7 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
 
 // d = a b.
 __device__ __forceinline__ void mma_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
@@ -277,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
   float* sm_l = sm_m + kWarps * 8;
   float* sm_fl = reinterpret_cast<float*>(smem + S::FIN);       // [8] 1 / sum of the merged row
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::BAR);
-  long long* sm_total = reinterpret_cast<long long*>(smem + S::MISC);        // [0] R, [1] first slot of the range, counted from the start of *sm_start
+  long long* sm_total = reinterpret_cast<long long*>(smem + S::MISC);        // [0] R, [1] R0 in sequence *sm_start
   int* sm_start = reinterpret_cast<int*>(smem + S::MISC + 16);               // b of the start
   int* sm_ticket = sm_start + 1;
   int* sm_ranges = sm_start + 2;                                             // N
@@ -394,10 +393,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
   // short of registers, wants them only at every 16th.
   volatile uint32_t* where = reinterpret_cast<uint32_t*>(smem + S::WHERE) + warp * 8;
   auto keep = [&]() {
-    if (lane == 0) where[0] = w.b, where[1] = w.g, where[2] = w.slots, where[3] = done, where[4] = pos, where[5] = w.pairs;
+    if (lane == 0) {
+      where[0] = w.b, where[1] = w.g, where[2] = w.slots;
+      where[3] = done, where[4] = pos, where[5] = w.pairs;
+    }
     __syncwarp();
   };
-  auto recall = [&]() { w.b = where[0], w.g = where[1], w.slots = where[2], done = where[3], pos = where[4], w.pairs = where[5]; };
+  auto recall = [&]() {
+    w.b = where[0], w.g = where[1], w.slots = where[2];
+    done = where[3], pos = where[4], w.pairs = where[5];
+  };
   keep();
   uint32_t taken = 0;          // slots consumed
   uint32_t src = kNoRecord;    // lane's record of the current 16 pairs (index into the pool), or none
@@ -473,9 +478,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
     float o[NT][4];
     float l0 = 0.f, l1 = 0.f;
     float m0 = kLowest, m1 = kLowest;          // softmax references (log2 units) of heads 2 t, 2 t + 1
-    {
-    const uint32_t until = min(w.slots, done + (len - pos));       // of the row, in this range
-    const uint32_t head0 = static_cast<uint32_t>(w.b) * a.Hq + w.g * G;   // the group's first query head
+    const uint32_t stop = min(w.slots, done + (len - pos));        // of the row, in this range
+    const uint32_t first_head = static_cast<uint32_t>(w.b) * a.Hq + w.g * G;
 
     // Query operands: lane 4 g + t holds head g, channels 32 i + 8 t + e.  And
     // -8 times the head's group sums, cut into three bf16 numbers, as the
@@ -490,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
 #pragma unroll
       for (int i = 0; i < GR; ++i) {
         uint4 v = {0, 0, 0, 0};
-        if (g < G) v = *reinterpret_cast<const uint4*>(a.q + static_cast<size_t>(head0 + g) * D + 32 * i + 8 * t);
+        if (g < G) v = *reinterpret_cast<const uint4*>(a.q + static_cast<size_t>(first_head + g) * D + 32 * i + 8 * t);
         qf[i][0] = v.x;
         qf[i][1] = v.y;
         qf[i][2] = v.z;
@@ -544,8 +548,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
     }
 
     // The next row's query, for when it is its turn.
-    if (pos + (until - done) < len && lane < G * D / 64 && head0 + 2 * G <= static_cast<uint32_t>(a.B) * a.Hq)
-      asm volatile("prefetch.global.L1 [%0];" ::"l"(a.q + static_cast<size_t>(head0 + G) * D + lane * 64));
+    if (pos + (stop - done) < len && lane < G * D / 64 && first_head + 2 * G <= static_cast<uint32_t>(a.B) * a.Hq)
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(a.q + static_cast<size_t>(first_head + G) * D + lane * 64));
 
 #pragma unroll
     for (int m = 0; m < NT; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
@@ -560,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
       plain2 = v.plain2;
       plain3 = v.plain3;
     }
-    const int j_end = static_cast<int>(until);
+    const int j_end = static_cast<int>(stop);
     for (int j = static_cast<int>(done + skip); j < j_end && ok; j += kWarps, ++taken) {
       const uint32_t stage = taken & (kDepth - 1), parity = (taken / kDepth) & 1u;
       const uint32_t none = missing & 3u;
@@ -647,7 +651,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
           if (!live(u0 + 2 * t + 9)) sv1[r] &= 0x0000ffffu;
         }
       }
-      bool large = (((sv0[0] + kLarge) | (sv1[0] + kLarge) | (sv0[1] + kLarge) | (sv1[1] + kLarge)) & 0x80008000u) != 0;
+      const uint32_t carried = (sv0[0] + kLarge) | (sv1[0] + kLarge) | (sv0[1] + kLarge) | (sv1[1] + kLarge);
+      bool large = (carried & 0x80008000u) != 0;
       const float t0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
       const float t1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
       if (__any_sync(0xffffffffu, t0 > th0 || t1 > th1 || large)) {
@@ -727,7 +732,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
           }
         }
       }
-    }
     }
     recall();
     const uint32_t pairs = w.pairs, until = min(w.slots, done + (len - pos));
@@ -831,7 +835,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
         const int i = tid, h = 2 * (i & 3), gi = (i & 31) >> 2, m = i >> 5;
         const bool act = i < S::PART4 && h < G;
         static_assert(S::PART4 <= kThreads, "one float4 per thread");
-        auto part_of = [&](int c) { return part + static_cast<size_t>(c == 0 ? f0 : 2 * (first + c)) * S::PART4 + i; };
+        auto part_of = [&](int c) {
+          return part + static_cast<size_t>(c == 0 ? f0 : 2 * (first + c)) * S::PART4 + i;
+        };
         constexpr int kAhead = 8;
         float4 ahead[kAhead];
 #pragma unroll

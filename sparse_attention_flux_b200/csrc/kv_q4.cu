@@ -79,7 +79,8 @@ __device__ __forceinline__ Quant quantise8(const uint4& x) {
   // f / s by a product and one residual step (Markstein), two at a time: where
   // f / s is a float, the residual is exact and so is the result, whatever the last
   // bits of r; else it is off by a rounding or two, and no border is that near.
-  const unsigned long long r2 = pack2(r, r), s2 = pack2(-s, -s), m2 = pack2(12582920.f, 12582920.f);   // 1.5 * 2^23 + 8
+  const unsigned long long r2 = pack2(r, r), s2 = pack2(-s, -s);
+  const unsigned long long m2 = pack2(12582920.f, 12582920.f);      // 1.5 * 2^23 + 8
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const unsigned long long f = pack2(bf16lo_to_f32(w[i]), bf16hi_to_f32(w[i]));

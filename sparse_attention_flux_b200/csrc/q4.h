@@ -16,8 +16,7 @@
 //                      the code of e in the 4 bits at 16 (e & 1) + 4 (e >> 1),
 //                      the word rotated left by 3: lane 4 g + t of a warp reads
 //                      one 16-byte vector (d 128) per token, the A operand of
-//                      its row, and a code that sits in bits 3..6 of its half
-//                      is a bf16 mantissa without a shift;
+//                      its row, a pair of codes 16 bits apart;
 //   V codes   at 8 d   the 32-bit word at hi 4 d + (4 g + t) d/8 + 4 j holds
 //                      tokens 8 hi + 2 t (low half) and 8 hi + 2 t + 1 (high
 //                      half), channels g d/8 + 4 j + i, i < 4, code at 4 i of

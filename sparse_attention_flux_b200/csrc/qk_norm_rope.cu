@@ -142,8 +142,9 @@ __global__ void __launch_bounds__(32 * kWarps, 5) norm_rope_kernel(const NormRop
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             if (INTER) {
-              y0[i] = r * (i % 2 ? fmaf(x0[i - i % 2], b0[i], x0[i] * a0[i]) : fmaf(-x0[i + 1], b0[i], x0[i] * a0[i]));
-              y1[i] = r * (i % 2 ? fmaf(x1[i - i % 2], b1[i], x1[i] * a1[i]) : fmaf(-x1[i + 1], b1[i], x1[i] * a1[i]));
+              const float p0 = i % 2 ? x0[i ^ 1] : -x0[i ^ 1], p1 = i % 2 ? x1[i ^ 1] : -x1[i ^ 1];
+              y0[i] = r * fmaf(p0, b0[i], x0[i] * a0[i]);
+              y1[i] = r * fmaf(p1, b1[i], x1[i] * a1[i]);
             } else {
               y0[i] = r * fmaf(-x1[i], b0[i], x0[i] * a0[i]);
               y1[i] = r * fmaf(x0[i], b1[i], x1[i] * a1[i]);
