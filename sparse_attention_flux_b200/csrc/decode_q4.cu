@@ -7,12 +7,12 @@
 // instructions per record as possible.
 //
 // Work split.  The live records of all (sequence, kv head) rows, in pairs, are
-// laid end to end and cut into equal ranges, one per CTA (two CTAs per SM, one
-// wave), so a ragged batch loads every SM alike.  A row counts kRowCost empty
-// slots more than its pairs for what it costs beside them; without any, the CTA
-// that got a batch's short requests, 45 rows of one or two pairs, took 90 us of
-// a call whose others ended after 25.  Where the rows are alike and few, each is
-// cut by itself instead.  A CTA walks its range row by row; within a row its
+// laid end to end and cut into equal ranges, one per CTA (one wave), so a ragged
+// batch loads every SM alike.  A row counts kRowCost empty slots more than its
+// pairs for what it costs beside them; without any, the CTA that got a batch's
+// short requests, 45 rows of one or two pairs, took 90 us of a call whose others
+// ended after 25.  Where the rows are alike and few, each is cut by itself instead.
+// A CTA walks its range row by row; within a row its
 // warps take pairs in turn and merge at the row's end in shared memory.  A row
 // that crosses a range border (at most the first and the last of a CTA) leaves a
 // partial in the workspace; the CTA that delivers a row's last partial (a
@@ -50,32 +50,45 @@ namespace flux {
 
 namespace {
 
-constexpr int kWarps = 8;                   // per CTA; 16 per SM, 128 registers a thread
-constexpr int kThreads = 32 * kWarps;
+// Two shapes, 16 warps of 128 registers per SM each: 2 CTAs of 8 warps, or 1 of 16.
+// With no more rows than SMs the second: half the range borders and parts to merge
+// (an SA layer of 16 sequences, 8 kv heads: 18.0 us against 20.2; 65536 tokens FA:
+// 215 against 222; one sequence of 131072 tokens, 1 kv head: 21.8 against 33.7; but
+// 30.7 against 29.4 where the 16 are ragged up to 32768).  With more rows the first:
+// a row's merge holds up 8 warps, and the SM's other CTA goes on meanwhile (60
+// sequences up to 3000 tokens, 8 kv heads: 18.4 us against 25; 64 sequences SA: 49
+// against 56); nor do 16 warps help rows of a few pairs (100 tokens: 7.0 against 5.9).
+template <int W>
+struct Shape {
+  static constexpr int kThreads = 32 * W;
+  static constexpr int kCtasPerSm = 16 / W;
+  // What a row costs beside its pairs, in pairs.  A ragged batch of 16 up to 32768
+  // tokens, 8 kv heads: 37.5, 32.5, 32.4, 32.6 us with 8, 14, 20, 28 at 8 warps;
+  // 31.2, 30.3, 30.6, 33.7 with 32, 48, 64, 96 at 16.
+  static constexpr int kRowCost = W == 16 ? 48 : 16;
+};
+constexpr int kComb = 10240;                // of the merge buffer: the weights of 320 parts come before
 constexpr int kDepth = 2;                   // ring stages of a warp, a pair of records each
-constexpr int kStages = kDepth * kWarps;
-constexpr int kRowCost = 16;                // what a row costs beside its pairs, in pairs: a ragged batch of 16
-                                            // up to 32768 tokens took 37.5, 32.5, 32.4, 32.6 us with 8, 14, 20, 28
 constexpr uint32_t kNoRecord = 0xffffffffu;
-constexpr int kCtasPerSm = 2;
+constexpr int kMergeCost = 24;              // of a row in parts (3 us), in pairs of a range
 constexpr float kGrow = 8.f;                // log2 growth of a score that is tolerated
 constexpr float kLowest = -3.0e38f;         // reference of a row without tokens: finite, so that
                                             // no difference of two references is NaN
 
 // Raw accumulator order: float4 (tile m, lane 4 g + t) = channels g D/8 + 2 m
 // and + 1 of heads 2 t and 2 t + 1, as the MMA leaves them.
-template <int D>
+template <int D, int W>
 struct Q4Smem {
   static constexpr int NT = D / 16;                       // channel tiles
-  static constexpr int RING = kStages * 2 * Q4Layout<D>::BYTES;
+  static constexpr int RING = W * kDepth * 2 * Q4Layout<D>::BYTES;
   static constexpr int PART4 = NT * 32;                   // float4 per partial
-  static constexpr int ACC = kWarps * PART4 * 16;
+  static constexpr int ACC = W * PART4 * 16;
   static constexpr int ML = RING + ACC;                   // m, l [warp][8]
-  static constexpr int FIN = ML + 2 * kWarps * 8 * 4;     // 1 / l of the final merge
+  static constexpr int FIN = ML + 2 * W * 8 * 4;     // 1 / l of the final merge
   static constexpr int BAR = FIN + 8 * 4;
-  static constexpr int MISC = BAR + kStages * 8;          // start row, totals, ticket
+  static constexpr int MISC = BAR + W * kDepth * 8;          // start row, totals, ticket
   static constexpr int WHERE = MISC + 64;                 // where each warp is
-  static constexpr int BYTES = WHERE + kWarps * 32;
+  static constexpr int BYTES = WHERE + W * 32;
 };
 
 // The live records of one sequence: [0, head) and [tail, end) of its records;
@@ -120,12 +133,12 @@ __device__ __forceinline__ Live live_of(const DecodeQ4Launch& a, int b, bool fa)
 }
 
 // How the rows are laid end to end: each row's pairs and some empty slots.
-// even == 0: a row has kRowCost empty slots; else every row has `even` slots.
+// even == 0: a row has `cost` empty slots; else every row has `even` slots.
 struct Plan {
-  uint32_t even;
+  uint32_t even, cost;
 };
 __device__ __forceinline__ uint32_t slots_of(const Plan& p, uint32_t pairs) {
-  return pairs == 0 ? 0u : p.even ? p.even : pairs + kRowCost;
+  return pairs == 0 ? 0u : p.even ? p.even : pairs + p.cost;
 }
 
 // Row (b, g), its pairs and its slots; rows without records are skipped.
@@ -265,15 +278,17 @@ __device__ __forceinline__ int cta_of(const Cuts& c, long long x) {
   return static_cast<int>(x < wide ? div_of(x, c.q + 1) : c.rem + div_of(x - wide, c.q));
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const DecodeQ4Launch a) {
+template <int D, int W>
+__global__ void __launch_bounds__(Shape<W>::kThreads, Shape<W>::kCtasPerSm)
+    decode_q4_kernel(const DecodeQ4Launch a) {
   using L = Q4Layout<D>;
-  using S = Q4Smem<D>;
+  using S = Q4Smem<D, W>;
+  constexpr int kThreads = Shape<W>::kThreads, kRowCost = Shape<W>::kRowCost;
   constexpr int NT = S::NT, GR = L::G;
   extern __shared__ __align__(128) uint8_t smem[];
   float4* sm_acc = reinterpret_cast<float4*>(smem + S::RING);
   float* sm_m = reinterpret_cast<float*>(smem + S::ML);
-  float* sm_l = sm_m + kWarps * 8;
+  float* sm_l = sm_m + W * 8;
   float* sm_fl = reinterpret_cast<float*>(smem + S::FIN);       // [8] 1 / sum of the merged row
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::BAR);
   long long* sm_total = reinterpret_cast<long long*>(smem + S::MISC);        // [0] R, [1] R0 in sequence *sm_start
@@ -282,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
   int* sm_ranges = sm_start + 2;                                             // N
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-  if (tid < kStages) mbar_init(full + tid, 1);
+  if (tid < W * kDepth) mbar_init(full + tid, 1);
   fence_barrier_init();
   griddep_launch_dependents();
   griddep_wait();
@@ -310,8 +325,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
     if (lane >= s) incl += x;
   }
   longest = __reduce_max_sync(0xffffffffu, longest);
-  long long* wsum = reinterpret_cast<long long*>(sm_acc);        // [kWarps], and the longest
-  uint32_t* wmax = reinterpret_cast<uint32_t*>(wsum + kWarps);
+  long long* wsum = reinterpret_cast<long long*>(sm_acc);        // [W], and the longest
+  uint32_t* wmax = reinterpret_cast<uint32_t*>(wsum + W);
   if (lane == 31) {
     wsum[warp] = incl;
     wmax[warp] = longest;
@@ -319,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
   __syncthreads();
   long long before = incl - mine, all = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < W; ++w) {
     const long long x = wsum[w];
     if (w < warp) before += x;
     all += x;
@@ -328,18 +343,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
   constexpr long long kSlotMask = (1LL << kCountBit) - 1;
   const int grid = gridDim.x, cta = blockIdx.x;
   const long long rows = (all >> kCountBit) * a.Hkv;
-  Plan plan = {0u};
+  Plan plan = {0u, kRowCost};
   Cuts cuts = {};
   long long R = all & kSlotMask, at0 = before & kSlotMask, n0 = mine & kSlotMask;
-  int N = static_cast<int>(min(static_cast<long long>(grid), (R + kWarps - 1) / kWarps));
+  int N = static_cast<int>(min(static_cast<long long>(grid), (R + W - 1) / W));
   if (rows > 0 && rows <= grid) {
-    // Every row in k equal parts, if the longest of them is no longer than an
-    // equal share of everything and a row's cost: then no CTA has two rows to
-    // merge (an SA layer, a batch of equal lengths).
+    // Every row by itself, in k equal parts or, up to three pairs a warp, whole; if
+    // that is no longer than an equal share of everything, with what the merges cost
+    // (an SA layer, a batch of equal lengths, few requests).
     const uint32_t k = static_cast<uint32_t>(grid) / static_cast<uint32_t>(rows);
-    const uint32_t part = max((longest + k - 1) / k, static_cast<uint32_t>(kWarps));
-    if (static_cast<long long>(part) * grid <= R + static_cast<long long>(kRowCost) * grid) {
-      const uint32_t parts = (longest + part - 1) / part;
+    const uint32_t part = longest <= 3 * W ? longest : max((longest + k - 1) / k, static_cast<uint32_t>(W));
+    const uint32_t parts = (longest + part - 1) / part;
+    const int cost = static_cast<int>(part) + (parts > 1 ? kMergeCost : 0) - 3 * kMergeCost / 2;
+    if (static_cast<long long>(cost) * grid <= max(R, static_cast<long long>(W) * grid)) {
       plan.even = part * parts;
       R = rows * plan.even;
       N = static_cast<int>(rows * parts);
@@ -384,11 +400,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
     done = static_cast<uint32_t>(off - static_cast<long long>(w.g) * w.slots);
   }
   // ---- the warp's stream of slots ---------------------------------------------
-  // Slot n of the warp is number warp + kWarps n of the CTA's range and goes
+  // Slot n of the warp is number warp + W n of the CTA's range and goes
   // to stage n mod kDepth of the warp's ring.
   uint8_t* ring = smem + warp * kDepth * 2 * L::BYTES;
   uint64_t* bars = full + warp * kDepth;
-  const uint32_t total = (len + kWarps - 1 - warp) / kWarps;
+  const uint32_t total = (len + W - 1 - warp) / W;
   // Row, done and pos stand in shared memory too: the loop over pairs, which is
   // short of registers, wants them only at every 16th.
   volatile uint32_t* where = reinterpret_cast<uint32_t*>(smem + S::WHERE) + warp * 8;
@@ -414,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
       src = kNoRecord;
       const uint32_t nl = n + (lane >> 1);
       if (nl < total) {
-        uint32_t x = where[3] + (warp + kWarps * nl - where[4]);   // counted from the row's start
+        uint32_t x = where[3] + (warp + W * nl - where[4]);   // counted from the row's start
         Row t;
         t.b = where[0], t.g = where[1], t.slots = where[2];
         while (x >= t.slots) {
@@ -555,8 +571,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
     for (int m = 0; m < NT; ++m) o[m][0] = o[m][1] = o[m][2] = o[m][3] = 0.f;
     float th0 = kLowest, th1 = kLowest;        // a score (before the scale) above it moves the reference
 
-    // The warp takes every kWarps-th slot of the CTA's range.
-    const uint32_t skip = (warp - pos) % kWarps;
+    // The warp takes every W-th slot of the CTA's range.
+    const uint32_t skip = (warp - pos) % W;
     int plain1, plain2, plain3;
     {
       const Live v = live_of(a, w.b, fa);
@@ -565,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
       plain3 = v.plain3;
     }
     const int j_end = static_cast<int>(stop);
-    for (int j = static_cast<int>(done + skip); j < j_end && ok; j += kWarps, ++taken) {
+    for (int j = static_cast<int>(done + skip); j < j_end && ok; j += W, ++taken) {
       const uint32_t stage = taken & (kDepth - 1), parity = (taken / kDepth) & 1u;
       const uint32_t none = missing & 3u;
       missing >>= 2;
@@ -770,14 +786,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
       if (h >= G) continue;
       float M0 = kLowest, M1 = kLowest;
 #pragma unroll
-      for (int v = 0; v < kWarps; ++v) {
+      for (int v = 0; v < W; ++v) {
         M0 = fmaxf(M0, sm_m[v * 8 + h]);
         M1 = fmaxf(M1, sm_m[v * 8 + h + 1]);
       }
       float ls0 = 0.f, ls1 = 0.f;
       float4 r = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int v = 0; v < kWarps; ++v) {
+      for (int v = 0; v < W; ++v) {
         const float w0 = ex2(sm_m[v * 8 + h] - M0), w1 = ex2(sm_m[v * 8 + h + 1] - M1);
         const float4 c = sm_acc[v * S::PART4 + i];
         ls0 = fmaf(w0, sm_l[v * 8 + h], ls0);
@@ -831,18 +847,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
         const int f0 = 2 * first + 1;
         float* wt = reinterpret_cast<float*>(sm_acc);              // [part][8] weights
         const int np = last - first + 1;
-        // A thread's float4 of the first parts, while the weights are worked out.
-        const int i = tid, h = 2 * (i & 3), gi = (i & 31) >> 2, m = i >> 5;
-        const bool act = i < S::PART4 && h < G;
-        static_assert(S::PART4 <= kThreads, "one float4 per thread");
+        // The parts are shared out to NG groups of threads, a float4 per thread.  The
+        // first ones are loaded while the weights are worked out.
+        constexpr int NG = kThreads / S::PART4, kAhead = 8;
+        static_assert(NG >= 1 && kThreads % S::PART4 == 0 && kComb + NG * S::PART4 * 16 <= S::ACC, "merge layout");
+        const int i = tid % S::PART4, group = tid / S::PART4;
+        const int h = 2 * (i & 3), gi = (i & 31) >> 2, m = i >> 5;
+        const bool act = h < G;
         auto part_of = [&](int c) {
           return part + static_cast<size_t>(c == 0 ? f0 : 2 * (first + c)) * S::PART4 + i;
         };
-        constexpr int kAhead = 8;
         float4 ahead[kAhead];
 #pragma unroll
         for (int c = 0; c < kAhead; ++c)
-          ahead[c] = act && c < np ? __ldcg(part_of(c)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          ahead[c] = act && c * NG + group < np ? __ldcg(part_of(c * NG + group)) : make_float4(0.f, 0.f, 0.f, 0.f);
         // Warp v: the weights of head v's parts, and the row's sum.
         if (warp < G) {
           float M = kLowest, ls = 0.f;
@@ -870,8 +888,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
           }
         }
         named_bar_sync(1, kThreads);
+        float4 r = {0.f, 0.f, 0.f, 0.f};
         if (act) {
-          float4 r = {0.f, 0.f, 0.f, 0.f};
           auto add = [&](int c, const float4& v) {
             const float w0 = wt[c * 8 + h], w1 = h + 1 < G ? wt[c * 8 + h + 1] : 0.f;
             r.x = fmaf(w0, v.x, r.x);
@@ -881,9 +899,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
           };
 #pragma unroll
           for (int c = 0; c < kAhead; ++c)
-            if (c < np) add(c, ahead[c]);
+            if (c * NG + group < np) add(c * NG + group, ahead[c]);
 #pragma unroll 8
-          for (int c = kAhead; c < np; ++c) add(c, __ldcg(part_of(c)));
+          for (int c = kAhead * NG + group; c < np; c += NG) add(c, __ldcg(part_of(c)));
+        }
+        if (NG > 1) {
+          float4* comb = sm_acc + kComb / 16;
+          comb[tid] = r;
+          named_bar_sync(1, kThreads);
+          if (group == 0) {
+#pragma unroll
+            for (int k = 1; k < NG; ++k) {
+              const float4 v = comb[k * S::PART4 + i];
+              r = make_float4(r.x + v.x, r.y + v.y, r.z + v.z, r.w + v.w);
+            }
+          }
+        }
+        if (act && group == 0) {
           const float i0 = sm_fl[h], i1 = h + 1 < G ? sm_fl[h + 1] : 0.f;
           uint16_t* out = a.o + static_cast<size_t>(head0 + h) * D + gi * (D / 8) + 2 * m;
           *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(r.x * i0, r.z * i0);
@@ -901,14 +933,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_q4_kernel(const D
   }
 }
 
-template <int D>
+template <int D, int W>
 cudaError_t launch_t(const DecodeQ4Launch& p, int num_sms, cudaStream_t stream) {
-  constexpr int smem = Q4Smem<D>::BYTES;
-  cudaError_t e = cudaFuncSetAttribute(decode_q4_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  constexpr int smem = Q4Smem<D, W>::BYTES;
+  static_assert(smem * Shape<W>::kCtasPerSm <= 226 << 10, "shared memory");
+  cudaError_t e =
+      cudaFuncSetAttribute(decode_q4_kernel<D, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kCtasPerSm * num_sms);
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(Shape<W>::kCtasPerSm * num_sms);
+  cfg.blockDim = dim3(Shape<W>::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -916,19 +950,30 @@ cudaError_t launch_t(const DecodeQ4Launch& p, int num_sms, cudaStream_t stream) 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_q4_kernel<D>, p);
+  return cudaLaunchKernelEx(&cfg, decode_q4_kernel<D, W>, p);
+}
+
+template <int D>
+cudaError_t launch_d(const DecodeQ4Launch& p, int num_sms, cudaStream_t stream) {
+  // At most one row per SM; of some length, and if they are few, of a length that is
+  // cut into many parts either way (8 rows of 1200 tokens: 9.6 us by 8 warps, 11.2 by
+  // 16; 64 rows of 300: 8.9 and 7.9).
+  const long long rows = static_cast<long long>(p.B) * p.Hkv;
+  const long long longest = static_cast<long long>(p.max_pages) * p.page_size;
+  const bool wide = rows <= num_sms && longest > (rows >= 32 ? 256 : 8192);
+  return wide ? launch_t<D, 16>(p, num_sms, stream) : launch_t<D, 8>(p, num_sms, stream);
 }
 
 }  // namespace
 
-// Two partials per CTA: float4 accumulators, m and l of 8 heads.
+// Two partials per CTA, of either shape: float4 accumulators, m and l of 8 heads.
 size_t decode_q4_workspace_bytes(int d, int num_sms) {
-  const size_t parts = static_cast<size_t>(2) * kCtasPerSm * num_sms;
+  const size_t parts = static_cast<size_t>(2) * Shape<8>::kCtasPerSm * num_sms;
   return parts * (static_cast<size_t>(d) / 16 * 32 * 16 + 2 * 8 * 4);
 }
 
 cudaError_t launch_decode_q4(const DecodeQ4Launch& p, int num_sms, cudaStream_t stream) {
-  return p.d == 64 ? launch_t<64>(p, num_sms, stream) : launch_t<128>(p, num_sms, stream);
+  return p.d == 64 ? launch_d<64>(p, num_sms, stream) : launch_d<128>(p, num_sms, stream);
 }
 
 }  // namespace flux

@@ -97,6 +97,25 @@ def test_long_and_ragged_requests(ctx, d, Hq, Hkv, page, lens, fa):
     c.check(q, o, lse, fa)
 
 
+@pytest.mark.parametrize("d,Hq,Hkv", [(64, 4, 2), (128, 8, 2), (128, 7, 7)])
+@pytest.mark.parametrize("fa", [True, False])
+@pytest.mark.parametrize("alike", [True, False])
+def test_more_rows_than_sms(ctx, d, Hq, Hkv, fa, alike):
+    """Up to three times as many (request, kv head) rows as SMs; all of one length, or ragged
+    with empty ones and a long one."""
+    B = 80 if Hkv == 2 else 50
+    lens = [333] * B if alike else np.random.default_rng(d).integers(0, 400, B).tolist()
+    if not alike:
+        lens[3], lens[40] = 6000, 0
+    c = Cache(ctx, lens, Hkv, d, 32, seed=24)
+    q = normal((B, Hq, d), 25)
+    o, lse = c.decode(ctx, q, fa, 1, 2, 64)
+    ctx.check()
+    c.check(q, o, lse, fa, 1, 2, 64)
+    again = c.decode(ctx, q, fa, 1, 2, 64)
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+
+
 @pytest.mark.parametrize("B,n", [(300, 1), (700, 40), (129, 200), (4096, 3)])
 def test_many_short_requests(ctx, B, n):
     g = np.random.default_rng(B)
