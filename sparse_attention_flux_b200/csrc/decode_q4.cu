@@ -12,11 +12,11 @@
 // pairs for what it costs beside them; without any, the CTA that got a batch's
 // short requests, 45 rows of one or two pairs, took 90 us of a call whose others
 // ended after 25.  Where the rows are alike and few, each is cut by itself instead.
-// A CTA walks its range row by row; within a row its
-// warps take pairs in turn and merge at the row's end in shared memory.  A row
-// that crosses a range border (at most the first and the last of a CTA) leaves a
-// partial in the workspace; the CTA that delivers a row's last partial (a
-// ticket) merges them in range order, so the result does not depend on timing.
+// A CTA walks its range row by row; within a row its warps take pairs in turn and
+// merge at the row's end in shared memory.  A row that crosses a range border (at
+// most the first and the last of a CTA) leaves a partial in the workspace; the CTA
+// that delivers a row's last partial (a ticket) merges them in range order, so the
+// result does not depend on timing.
 //
 // Stream.  Records are taken in pairs.  Each warp keeps a ring of two pairs in
 // shared memory, filled by bulk copies (one, when the page holds both records):
@@ -409,6 +409,7 @@ __global__ void __launch_bounds__(Shape<W>::kThreads, Shape<W>::kCtasPerSm)
   // short of registers, wants them only at every 16th.
   volatile uint32_t* where = reinterpret_cast<uint32_t*>(smem + S::WHERE) + warp * 8;
   auto keep = [&]() {
+    __syncwarp();              // nobody recalls the old place any more
     if (lane == 0) {
       where[0] = w.b, where[1] = w.g, where[2] = w.slots;
       where[3] = done, where[4] = pos, where[5] = w.pairs;
