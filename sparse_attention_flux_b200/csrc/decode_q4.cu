@@ -36,8 +36,12 @@
 //     bits).
 //   O^T += V^T P^T: the lane's channels are the rows; u s - 8 s is one packed
 //     fma with s brought up by 2^108, and exactly the stored value times 2^-25.
-//     P is rounded to bf16 for the MMA (the softmax sum keeps fp32 values) and
-//     turned by movmatrix.
+//     The softmax sum keeps the weights P in fp32; the MMA takes them as two bf16
+//     pieces, 16 bits, so that the output's one rounding is the error left.  (One
+//     piece, 8 bits, made a batch's outputs 1.4 times as far off: 0.00234 against
+//     0.00166 in the mean.  The second costs 1-2 % of short calls, 4 % of long ones
+//     with up to 4 heads a group, where it rides in the operand's idle columns, and
+//     9 % with more.)  movmatrix turns them.
 // Unpacking by shift and AND-OR into 16 + u instead, seven or eight operations
 // for four pairs where these take six and five: 249 us against 224 (16 x 65536
 // tokens, 8 kv heads, d 128).
@@ -203,6 +207,55 @@ __device__ __forceinline__ void mma_zero(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
+// Two fp32 numbers in one operation.
+__device__ __forceinline__ unsigned long long bits_of(float2 x) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x.x), "f"(x.y));
+  return r;
+}
+__device__ __forceinline__ float2 pair_of(unsigned long long x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits_of(x)), "l"(bits_of(y)), "l"(bits_of(z)));
+  return pair_of(r);
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits_of(x)), "l"(bits_of(y)));
+  return pair_of(r);
+}
+
+// The weights of 8 tokens and the group's heads as the second operand of a value MMA,
+// in two bf16 pieces, p = high + low to 2^-16 of p.
+//   Paired (up to 4 heads): the query stands in the 8 columns twice, and column h + 4
+//     takes the low piece of head h; its accumulators join those of h where the
+//     warps merge.  minus is -1 in the lanes of those columns, else 0.
+//   Else the low pieces take an MMA of their own, and minus is -1.
+template <bool PAIRED>
+struct Weights {
+  uint32_t high, low;
+  __device__ __forceinline__ Weights(float2 p, float minus) {
+    high = pack_bf16x2(p.x, p.y);
+    const float2 rest = fma2(make_float2(minus, minus), make_float2(bf16lo_to_f32(high), bf16hi_to_f32(high)), p);
+    if constexpr (PAIRED) {
+      high = movmatrix_trans(pack_bf16x2(rest.x, rest.y));
+    } else {
+      low = movmatrix_trans(pack_bf16x2(rest.x, rest.y));
+      high = movmatrix_trans(high);
+    }
+  }
+};
+template <bool PAIRED>
+__device__ __forceinline__ void add_values(float (&d)[4], const uint32_t (&a)[4], const Weights<PAIRED>& b0,
+                                           const Weights<PAIRED>& b1) {
+  mma_add(d, a, b0.high, b1.high);
+  if constexpr (!PAIRED) mma_add(d, a, b0.low, b1.low);
+}
+
 // One lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
@@ -278,7 +331,7 @@ __device__ __forceinline__ int cta_of(const Cuts& c, long long x) {
   return static_cast<int>(x < wide ? div_of(x, c.q + 1) : c.rem + div_of(x - wide, c.q));
 }
 
-template <int D, int W>
+template <int D, int W, bool PAIRED>
 __global__ void __launch_bounds__(Shape<W>::kThreads, Shape<W>::kCtasPerSm)
     decode_q4_kernel(const DecodeQ4Launch a) {
   using L = Q4Layout<D>;
@@ -386,6 +439,7 @@ __global__ void __launch_bounds__(Shape<W>::kThreads, Shape<W>::kCtasPerSm)
   const int g = lane >> 2, t = lane & 3;
 
   const float sl2 = a.scale * 1.4426950408889634f;
+  const float minus = PAIRED && t < 2 ? 0.f : -1.f;       // of the weights' low pieces
   // The position in the range: row w, of which `done` slots are behind us, at
   // slot `pos` of the CTA's `len`.
   Row w = {};
@@ -493,12 +547,12 @@ __global__ void __launch_bounds__(Shape<W>::kThreads, Shape<W>::kCtasPerSm)
 
   while (pos < len) {
     float o[NT][4];
-    float l0 = 0.f, l1 = 0.f;
+    float2 l = {0.f, 0.f};
     float m0 = kLowest, m1 = kLowest;          // softmax references (log2 units) of heads 2 t, 2 t + 1
     const uint32_t stop = min(w.slots, done + (len - pos));        // of the row, in this range
     const uint32_t first_head = static_cast<uint32_t>(w.b) * a.Hq + w.g * G;
 
-    // Query operands: lane 4 g + t holds head g, channels 32 i + 8 t + e.  And
+    // Query operands: lane 4 g + t holds head g (paired: g mod 4), channels 32 i + 8 t + e.  And
     // -8 times the head's group sums, cut into three bf16 numbers, as the
     // second operand of an MMA whose first is the tokens' scales: row 2 t + e
     // of that product is (at d 128) piece t / 2 of group 2 (t % 2) + e, rows 8
@@ -511,7 +565,9 @@ __global__ void __launch_bounds__(Shape<W>::kThreads, Shape<W>::kCtasPerSm)
 #pragma unroll
       for (int i = 0; i < GR; ++i) {
         uint4 v = {0, 0, 0, 0};
-        if (g < G) v = *reinterpret_cast<const uint4*>(a.q + static_cast<size_t>(first_head + g) * D + 32 * i + 8 * t);
+        const int head = PAIRED ? g & 3 : g;
+        if (head < G)
+          v = *reinterpret_cast<const uint4*>(a.q + static_cast<size_t>(first_head + head) * D + 32 * i + 8 * t);
         qf[i][0] = v.x;
         qf[i][1] = v.y;
         qf[i][2] = v.z;
@@ -687,8 +743,8 @@ __global__ void __launch_bounds__(Shape<W>::kThreads, Shape<W>::kCtasPerSm)
         m1 = n1;
         th0 = (n0 + kGrow) / sc0;
         th1 = (n1 + kGrow) / sc1;
-        l0 *= f0;
-        l1 *= f1;
+        l.x *= f0;
+        l.y *= f1;
 #pragma unroll
         for (int m = 0; m < NT; ++m) {
           o[m][0] *= f0;
@@ -699,13 +755,11 @@ __global__ void __launch_bounds__(Shape<W>::kThreads, Shape<W>::kCtasPerSm)
       }
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float p00 = ex2(fmaf(x[r][0], sc0, -m0)), p01 = ex2(fmaf(x[r][1], sc1, -m1));
-        const float p10 = ex2(fmaf(x[r][2], sc0, -m0)), p11 = ex2(fmaf(x[r][3], sc1, -m1));
-        l0 += p00 + p10;
-        l1 += p01 + p11;
+        const float2 p0 = {ex2(fmaf(x[r][0], sc0, -m0)), ex2(fmaf(x[r][1], sc1, -m1))};
+        const float2 p1 = {ex2(fmaf(x[r][2], sc0, -m0)), ex2(fmaf(x[r][3], sc1, -m1))};
+        l = add2(l, add2(p0, p1));
         if (!large) {
-          const uint32_t b0 = movmatrix_trans(pack_bf16x2(p00, p01));
-          const uint32_t b1 = movmatrix_trans(pack_bf16x2(p10, p11));
+          const Weights<PAIRED> b0(p0, minus), b1(p1, minus);
           const uint32_t e0 = mul_bf16x2(sv0[r], kUpEven), e1 = mul_bf16x2(sv1[r], kUpEven);
           const uint32_t o0 = mul_bf16x2(sv0[r], kUpOdd), o1 = mul_bf16x2(sv1[r], kUpOdd);
           const uint32_t n0 = mul_bf16x2(sv0[r], kDown8), n1 = mul_bf16x2(sv1[r], kDown8);
@@ -715,20 +769,19 @@ __global__ void __launch_bounds__(Shape<W>::kThreads, Shape<W>::kCtasPerSm)
             {
               const uint32_t af[4] = {fma_bf16x2(fields<0>(y0), e0, n0), fma_bf16x2(fields<1>(y0), o0, n0),
                                       fma_bf16x2(fields<0>(y1), e1, n1), fma_bf16x2(fields<1>(y1), o1, n1)};
-              mma_add(o[2 * i], af, b0, b1);
+              add_values(o[2 * i], af, b0, b1);
             }
             {
               const uint32_t af[4] = {fma_bf16x2(fields<2>(z0), e0, n0), fma_bf16x2(fields<3>(z0), o0, n0),
                                       fma_bf16x2(fields<2>(z1), e1, n1), fma_bf16x2(fields<3>(z1), o1, n1)};
-              mma_add(o[2 * i + 1], af, b0, b1);
+              add_values(o[2 * i + 1], af, b0, b1);
             }
           }
         } else {
           // Large values: 16 + u from the mantissa, (16 + u) scale - 24 scale the
           // value itself, and 2^-25 on the other operand.
           const float f = 1.f / kValueUnit;
-          const uint32_t b0 = movmatrix_trans(pack_bf16x2(p00 * f, p01 * f));
-          const uint32_t b1 = movmatrix_trans(pack_bf16x2(p10 * f, p11 * f));
+          const Weights<PAIRED> b0(make_float2(p0.x * f, p0.y * f), minus), b1(make_float2(p1.x * f, p1.y * f), minus);
           const uint32_t n0 = mul_bf16x2(sv0[r], 0xc1c0c1c0u), n1 = mul_bf16x2(sv1[r], 0xc1c0c1c0u);   // -24
           auto value = [](uint32_t x, uint32_t scale, uint32_t n) {
             return fma_bf16x2((x & 0x00780078u) | 0x41804180u, scale, n);
@@ -739,12 +792,12 @@ __global__ void __launch_bounds__(Shape<W>::kThreads, Shape<W>::kCtasPerSm)
             {
               const uint32_t af[4] = {value(y0 << 3, sv0[r], n0), value(y0 >> 1, sv0[r], n0),
                                       value(y1 << 3, sv1[r], n1), value(y1 >> 1, sv1[r], n1)};
-              mma_add(o[2 * i], af, b0, b1);
+              add_values(o[2 * i], af, b0, b1);
             }
             {
               const uint32_t af[4] = {value(y0 >> 5, sv0[r], n0), value(y0 >> 9, sv0[r], n0),
                                       value(y1 >> 5, sv1[r], n1), value(y1 >> 9, sv1[r], n1)};
-              mma_add(o[2 * i + 1], af, b0, b1);
+              add_values(o[2 * i + 1], af, b0, b1);
             }
           }
         }
@@ -764,8 +817,8 @@ __global__ void __launch_bounds__(Shape<W>::kThreads, Shape<W>::kCtasPerSm)
     // ---- merge the warps --------------------------------------------------
 #pragma unroll
     for (int s = 4; s < 32; s <<= 1) {
-      l0 += __shfl_xor_sync(0xffffffffu, l0, s);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, s);
+      l.x += __shfl_xor_sync(0xffffffffu, l.x, s);
+      l.y += __shfl_xor_sync(0xffffffffu, l.y, s);
     }
 #pragma unroll
     for (int m = 0; m < NT; ++m)
@@ -773,8 +826,8 @@ __global__ void __launch_bounds__(Shape<W>::kThreads, Shape<W>::kCtasPerSm)
     if (g == 0) {
       sm_m[warp * 8 + 2 * t] = m0;
       sm_m[warp * 8 + 2 * t + 1] = m1;
-      sm_l[warp * 8 + 2 * t] = l0;
-      sm_l[warp * 8 + 2 * t + 1] = l1;
+      sm_l[warp * 8 + 2 * t] = l.x;
+      sm_l[warp * 8 + 2 * t + 1] = l.y;
     }
     const bool fine = named_bar_and(1, kThreads, ok);
     const bool whole = begins && ends;
@@ -783,8 +836,7 @@ __global__ void __launch_bounds__(Shape<W>::kThreads, Shape<W>::kCtasPerSm)
     float* part_m = a.part + static_cast<size_t>(2) * gridDim.x * S::PART4 * 4;
     float* part_l = part_m + 2 * gridDim.x * 8;
     for (int i = tid; i < S::PART4; i += kThreads) {
-      const int h = 2 * (i & 3), gi = (i & 31) >> 2, m = i >> 5;
-      if (h >= G) continue;
+      const int h = 2 * (PAIRED ? i & 1 : i & 3), gi = (i & 31) >> 2, m = i >> 5;
       float M0 = kLowest, M1 = kLowest;
 #pragma unroll
       for (int v = 0; v < W; ++v) {
@@ -804,6 +856,14 @@ __global__ void __launch_bounds__(Shape<W>::kThreads, Shape<W>::kCtasPerSm)
         r.z = fmaf(w0, c.z, r.z);
         r.w = fmaf(w1, c.w, r.w);
       }
+      if constexpr (PAIRED) {                  // high and low pieces
+        r.x += __shfl_xor_sync(0xffffffffu, r.x, 2);
+        r.y += __shfl_xor_sync(0xffffffffu, r.y, 2);
+        r.z += __shfl_xor_sync(0xffffffffu, r.z, 2);
+        r.w += __shfl_xor_sync(0xffffffffu, r.w, 2);
+        if (i & 2) continue;
+      }
+      if (h >= G) continue;
       if (!fine) {                             // a wait ran out: the row's output is zero
         ls0 = ls1 = whole ? 0.f : -1.f;
         r = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -934,12 +994,12 @@ __global__ void __launch_bounds__(Shape<W>::kThreads, Shape<W>::kCtasPerSm)
   }
 }
 
-template <int D, int W>
+template <int D, int W, bool PAIRED>
 cudaError_t launch_t(const DecodeQ4Launch& p, int num_sms, cudaStream_t stream) {
   constexpr int smem = Q4Smem<D, W>::BYTES;
   static_assert(smem * Shape<W>::kCtasPerSm <= 226 << 10, "shared memory");
   cudaError_t e =
-      cudaFuncSetAttribute(decode_q4_kernel<D, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      cudaFuncSetAttribute(decode_q4_kernel<D, W, PAIRED>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(Shape<W>::kCtasPerSm * num_sms);
@@ -951,7 +1011,7 @@ cudaError_t launch_t(const DecodeQ4Launch& p, int num_sms, cudaStream_t stream) 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_q4_kernel<D, W>, p);
+  return cudaLaunchKernelEx(&cfg, decode_q4_kernel<D, W, PAIRED>, p);
 }
 
 template <int D>
@@ -962,7 +1022,9 @@ cudaError_t launch_d(const DecodeQ4Launch& p, int num_sms, cudaStream_t stream) 
   const long long rows = static_cast<long long>(p.B) * p.Hkv;
   const long long longest = static_cast<long long>(p.max_pages) * p.page_size;
   const bool wide = rows <= num_sms && longest > (rows >= 32 ? 256 : 8192);
-  return wide ? launch_t<D, 16>(p, num_sms, stream) : launch_t<D, 8>(p, num_sms, stream);
+  if (p.Hq / p.Hkv <= 4)
+    return wide ? launch_t<D, 16, true>(p, num_sms, stream) : launch_t<D, 8, true>(p, num_sms, stream);
+  return wide ? launch_t<D, 16, false>(p, num_sms, stream) : launch_t<D, 8, false>(p, num_sms, stream);
 }
 
 }  // namespace
