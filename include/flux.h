@@ -44,7 +44,8 @@
  *     0 = SA), so routing and attention chain on one stream with no host sync.
  *   - A flux_ctx owns the only memory the library allocates (a workspace for
  *     split-KV decode partials and router intermediates, and the error word).
- *     Calls that share a ctx must not overlap in time on different streams.
+ *     Calls that share a ctx must not overlap in time on different streams
+ *     (flux_build_page_table may, beside calls of the others).
  *   - flux_last_error() describes the last failure of the calling thread.
  */
 #ifndef FLUX_H
@@ -428,6 +429,11 @@ int flux_decode_workspace_bytes(flux_ctx* ctx, int B, int Hq, int Hkv, int d, in
  * outside the list, nothing is handed out: the table and the cursor stay, all
  * slots are -1, cu_new is 0); a negative page id where one is needed (slot -1).
  * B <= 8192.
+ * Its CTAs are counted in a word of the ctx that no other call uses, so the next
+ * step's table may be built on a second stream beside the ctx's other calls (not
+ * beside another table).  The error word stays one: an error of either may end
+ * the other early, and flux_ctx_check, which then clears the ctx's counters,
+ * wants both streams idle.
  *
  * flux_qk_norm_rope: q and k of N tokens from the projection's output to what
  * the attention calls take.  Per head: y = x / sqrt(mean(x^2) + eps) * weight

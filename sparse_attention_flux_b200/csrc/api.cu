@@ -20,7 +20,8 @@ struct flux_ctx {
   int num_sms;
   void* workspace;        // scratch shared by the calls (they must not overlap in time)
   size_t workspace_bytes;
-  int* tickets;           // [kMaxTickets + 1] ints, zero between calls; last one: router
+  int* tickets;           // [kTicketWords] ints, zero between calls: merges of decode rows, then
+                          // the router's and the page tables' word
   int* err;               // device error word
   long long spin_ns;
 };
@@ -28,6 +29,7 @@ struct flux_ctx {
 namespace {
 
 constexpr int kMaxTickets = 1 << 16;
+constexpr int kRouterTicket = kMaxTickets, kPageTableTicket = kMaxTickets + 1, kTicketWords = kMaxTickets + 2;
 thread_local std::string g_last_error;
 
 int fail(int code, const char* fmt, ...) {
@@ -321,10 +323,10 @@ int flux_ctx_create(flux_ctx** out, int device, size_t workspace_bytes) {
     if (ms > 0) c->spin_ns = ms * 1000000LL;
   }
   if ((e = cudaMalloc(&c->workspace, c->workspace_bytes)) != cudaSuccess ||
-      (e = cudaMalloc(reinterpret_cast<void**>(&c->tickets), (kMaxTickets + 1) * sizeof(int))) !=
+      (e = cudaMalloc(reinterpret_cast<void**>(&c->tickets), kTicketWords * sizeof(int))) !=
           cudaSuccess ||
       (e = cudaMalloc(reinterpret_cast<void**>(&c->err), sizeof(int))) != cudaSuccess ||
-      (e = cudaMemset(c->tickets, 0, (kMaxTickets + 1) * sizeof(int))) != cudaSuccess ||
+      (e = cudaMemset(c->tickets, 0, kTicketWords * sizeof(int))) != cudaSuccess ||
       (e = cudaMemset(c->err, 0, sizeof(int))) != cudaSuccess ||
       (e = cudaDeviceSynchronize()) != cudaSuccess) {
     cudaFree(c->workspace);
@@ -363,7 +365,7 @@ int flux_ctx_check(flux_ctx* c, flux_stream_t stream) {
   if (word == flux::DEV_OK) return FLUX_OK;
   // Clear the word and any ticket an aborted kernel left behind.
   cudaMemset(c->err, 0, sizeof(int));
-  cudaMemset(c->tickets, 0, (kMaxTickets + 1) * sizeof(int));
+  cudaMemset(c->tickets, 0, kTicketWords * sizeof(int));
   cudaDeviceSynchronize();
   switch (word) {
     case flux::DEV_ERR_TIMEOUT:
@@ -413,7 +415,7 @@ int flux_route(flux_ctx* c, const uint16_t* hidden, int T, int Hd, int n_pool, c
   p.score = score;
   p.pooled = static_cast<float*>(c->workspace);
   p.hidden1 = p.pooled + flux::route_hidden1_offset(Hd);
-  p.ticket = c->tickets + kMaxTickets;
+  p.ticket = c->tickets + kRouterTicket;
   const cudaError_t e = flux::launch_route(p, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FLUX_OK : cuda_fail(e, "flux_route: launch");
 }
@@ -789,7 +791,7 @@ extern "C" int flux_build_page_table(flux_ctx* c, const int32_t* old_lens, const
   if (rc != FLUX_OK) return rc;
   const flux::PageTableLaunch p{old_lens, new_lens, B, page_size, sink_pages, window_pages,
                                 free_pages, n_free, cursor, cursor_out, page_table, max_pages,
-                                slots, positions, n_slots, cu_new, c->tickets, c->err};
+                                slots, positions, n_slots, cu_new, c->tickets + kPageTableTicket, c->err};
   const cudaError_t e = flux::launch_page_table(p, c->num_sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FLUX_OK : cuda_fail(e, name);
 }
