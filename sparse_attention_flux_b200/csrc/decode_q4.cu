@@ -71,7 +71,8 @@ struct Shape {
   // 31.2, 30.3, 30.6, 33.7 with 32, 48, 64, 96 at 16.
   static constexpr int kRowCost = W == 16 ? 48 : 16;
 };
-constexpr int kComb = 10240;                // of the merge buffer: the weights of 320 parts come before
+constexpr int kMaxParts = 320;              // of a row, so of CTAs: the merge buffer begins with their weights
+constexpr int kComb = kMaxParts * 8 * 4;    // (a full die pair has 160 SMs)
 constexpr int kDepth = 2;                   // ring stages of a warp, a pair of records each
 constexpr uint32_t kNoRecord = 0xffffffffu;
 constexpr int kMergeCost = 24;              // of a row in parts (3 us), in pairs of a range
@@ -994,6 +995,11 @@ __global__ void __launch_bounds__(Shape<W>::kThreads, Shape<W>::kCtasPerSm)
   }
 }
 
+template <int W>
+int ctas_of(int num_sms) {
+  return min(Shape<W>::kCtasPerSm * num_sms, kMaxParts);
+}
+
 template <int D, int W, bool PAIRED>
 cudaError_t launch_t(const DecodeQ4Launch& p, int num_sms, cudaStream_t stream) {
   constexpr int smem = Q4Smem<D, W>::BYTES;
@@ -1002,7 +1008,7 @@ cudaError_t launch_t(const DecodeQ4Launch& p, int num_sms, cudaStream_t stream) 
       cudaFuncSetAttribute(decode_q4_kernel<D, W, PAIRED>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(Shape<W>::kCtasPerSm * num_sms);
+  cfg.gridDim = dim3(ctas_of<W>(num_sms));
   cfg.blockDim = dim3(Shape<W>::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -1031,7 +1037,7 @@ cudaError_t launch_d(const DecodeQ4Launch& p, int num_sms, cudaStream_t stream) 
 
 // Two partials per CTA, of either shape: float4 accumulators, m and l of 8 heads.
 size_t decode_q4_workspace_bytes(int d, int num_sms) {
-  const size_t parts = static_cast<size_t>(2) * Shape<8>::kCtasPerSm * num_sms;
+  const size_t parts = static_cast<size_t>(2) * ctas_of<8>(num_sms);
   return parts * (static_cast<size_t>(d) / 16 * 32 * 16 + 2 * 8 * 4);
 }
 
