@@ -462,7 +462,8 @@ int flux_decode_workspace_bytes(flux_ctx* ctx, int B, int Hq, int Hkv, int d, in
  * tokens are read is a device-checked error and leaves those tokens out; other
  * entries are never read.  Bytes behind a sequence's last token are never
  * used, whatever they hold.  q, o, lse, layer_mode, sink / window / block,
- * scale and the group limits as flux_attn_decode.  |q| below 2^120.  Split
+ * and the group limits as flux_attn_decode.  |q| and scale * |q| below 2^120,
+ * scale at most 2^120 (INVALID_ARG), scores within fp32's range.  Split
  * partials live in the ctx workspace (flux_decode_q4_workspace_bytes). */
 int flux_build_page_table(flux_ctx* ctx, const int32_t* old_lens, const int32_t* new_lens, int B,
                           int page_size, int sink_pages, int window_pages,

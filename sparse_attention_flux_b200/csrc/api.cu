@@ -902,8 +902,9 @@ extern "C" int flux_attn_decode_q4(flux_ctx* c, const uint16_t* q, const uint8_t
   if (block < 1 || sink_blocks < 0 || window_blocks < 1)
     return fail(FLUX_ERR_INVALID_ARG, "%s: bad block / sink / window", name);
   if (layer_mode && layer < 0) return fail(FLUX_ERR_INVALID_ARG, "%s: negative layer", name);
-  if (!(scale == scale) || scale <= 0.f || scale > 3.0e38f)
-    return fail(FLUX_ERR_INVALID_ARG, "%s: scale must be finite and positive", name);
+  // Above 2^120 the factor that takes a score to log2 units, 2^7 scale log2(e) for a query of 1, is infinite.
+  if (!(scale > 0.f) || scale > 0x1p120f)
+    return fail(FLUX_ERR_INVALID_ARG, "%s: scale must be positive and at most 2^120", name);
   if (static_cast<long long>(B) * Hkv > kMaxTickets)
     return fail(FLUX_ERR_SHAPE, "%s: B * Hkv = %lld exceeds %d", name,
                 static_cast<long long>(B) * Hkv, kMaxTickets);
