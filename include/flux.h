@@ -463,7 +463,10 @@ int flux_decode_workspace_bytes(flux_ctx* ctx, int B, int Hq, int Hkv, int d, in
  * entries are never read.  Bytes behind a sequence's last token are never
  * used, whatever they hold.  q, o, lse, layer_mode, sink / window / block,
  * and the group limits as flux_attn_decode.  |q| and scale * |q| below 2^120,
- * scale at most 2^120 (INVALID_ARG), scores within fp32's range.  Split
+ * scale at most 2^120 (INVALID_ARG), scores within fp32's range.  The same call
+ * gives the same bits; a table of another width may give others (sums in another
+ * order: max_pages * page_size is the bound of the lengths by which the launch
+ * is shaped, and one far above them can cost short requests 1 to 2 us).  Split
  * partials live in the ctx workspace (flux_decode_q4_workspace_bytes). */
 int flux_build_page_table(flux_ctx* ctx, const int32_t* old_lens, const int32_t* new_lens, int B,
                           int page_size, int sink_pages, int window_pages,

@@ -44,7 +44,7 @@
 //     9 % with more.)  movmatrix turns them.
 // Unpacking by shift and AND-OR into 16 + u instead, seven or eight operations
 // for four pairs where these take six and five: 249 us against 224 (16 x 65536
-// tokens, 8 kv heads, d 128).
+// tokens, 8 kv heads, d 128; both with P in one piece).
 // The softmax runs against a reference that only grows when a score passes it
 // by 8 (in log2 units): p <= 2^8, and the common record needs no rescaling and
 // one vote.
@@ -56,19 +56,21 @@ namespace {
 
 // Two shapes, 16 warps of 128 registers per SM each: 2 CTAs of 8 warps, or 1 of 16.
 // With no more rows than SMs the second: half the range borders and parts to merge
-// (an SA layer of 16 sequences, 8 kv heads: 18.0 us against 20.2; 65536 tokens FA:
-// 215 against 222; one sequence of 131072 tokens, 1 kv head: 21.8 against 33.7; but
-// 30.7 against 29.4 where the 16 are ragged up to 32768).  With more rows the first:
-// a row's merge holds up 8 warps, and the SM's other CTA goes on meanwhile (60
-// sequences up to 3000 tokens, 8 kv heads: 18.4 us against 25; 64 sequences SA: 49
-// against 56); nor do 16 warps help rows of a few pairs (100 tokens: 7.0 against 5.9).
+// (an SA layer of 16 sequences, 8 kv heads: 18.3 us against 20.6; 65536 tokens FA:
+// 224-242 against 232-250; one sequence of 131072 tokens, 1 kv head: 21.1 against 32.4;
+// but 31.3 against 30.1 where the 16 are ragged up to 32768, and 14.5 against 13.0 where
+// 24 are up to 9000, 4 kv heads, d 64).  With more rows the first: a row's merge holds
+// up 8 warps, and the SM's other CTA goes on meanwhile (60 sequences up to 3000 tokens,
+// 8 kv heads: 23.7 us against 34.3; 64 sequences SA: 50 against 59); nor do 16 warps help
+// rows of a few pairs (100 tokens: 7.1 against 6.0).
 template <int W>
 struct Shape {
   static constexpr int kThreads = 32 * W;
   static constexpr int kCtasPerSm = 16 / W;
   // What a row costs beside its pairs, in pairs.  A ragged batch of 16 up to 32768
-  // tokens, 8 kv heads: 37.5, 32.5, 32.4, 32.6 us with 8, 14, 20, 28 at 8 warps;
-  // 31.2, 30.3, 30.6, 33.7 with 32, 48, 64, 96 at 16.
+  // tokens, 8 kv heads: 38.1, 30.5, 30.1, 30.1, 30.6 us with 8, 14, 16, 20, 28 at 8
+  // warps; 32.3, 31.3, 32.0, 35.2 with 32, 48, 64, 96 at 16.  One of 24 up to 9000, 4 kv
+  // heads, d 64: 14.8, 14.5, 14.5 with 32, 48, 64 at 16.
   static constexpr int kRowCost = W == 16 ? 48 : 16;
 };
 constexpr int kMaxParts = 320;              // of a row, so of CTAs: the merge buffer begins with their weights
@@ -1023,8 +1025,12 @@ cudaError_t launch_t(const DecodeQ4Launch& p, int num_sms, cudaStream_t stream) 
 template <int D>
 cudaError_t launch_d(const DecodeQ4Launch& p, int num_sms, cudaStream_t stream) {
   // At most one row per SM; of some length, and if they are few, of a length that is
-  // cut into many parts either way (8 rows of 1200 tokens: 9.6 us by 8 warps, 11.2 by
-  // 16; 64 rows of 300: 8.9 and 7.9).
+  // cut into many parts either way (8 rows of 1200 tokens: 9.6 us by 8 warps, 11.3 by
+  // 16; 64 rows of 300: 9.1 and 8.0).  The lengths are on the device: the bound that the
+  // host has is the table's capacity.  A table wider than its requests need takes the
+  // second shape for short ones too: up to 16 rows, 5.7-6.1 us become 6.8-7.2 at 100
+  // tokens, 8.9-10.6 become 11.1-11.4 at 1200, and from 4000 (one row: 9000) tokens on,
+  // or with 64 rows from 300 on, there is no difference.
   const long long rows = static_cast<long long>(p.B) * p.Hkv;
   const long long longest = static_cast<long long>(p.max_pages) * p.page_size;
   const bool wide = rows <= num_sms && longest > (rows >= 32 ? 256 : 8192);

@@ -14,7 +14,8 @@
 // multiplied into the weights, which leaves three operations a channel.  32768
 // tokens, 32 + 8 heads, d 128: 118 us, 5.7 TB/s of 671 MB (weights and sines
 // applied one after the other, no early loads: 136 us; 4 CTAs per SM without
-// the register limit 124, 6 with it 121-123).
+// the register limit 124, 6 with it 121-123; the limit of 5 spills 12 registers
+// of the half-split form).
 #include "q4.h"
 
 namespace flux {

@@ -571,7 +571,9 @@ class Context:
                        layer: int = 0, sink_blocks: int = 1, window_blocks: int = 16,
                        block: int = 128, lse=None, stream=None):
         """attn_decode over a paged 4-bit cache: token u of sequence b is in page
-        page_table[b, u // page_size] of kv_pool."""
+        page_table[b, u // page_size] of kv_pool.  The launch is shaped by the table's width, the
+        only bound of the lengths on the host: a table much wider than short requests need costs
+        them 1 to 2 us, and may change the last bits."""
         q_at = _at(q, self._bf16, "q", self)
         o_at = _at(o, self._bf16, "o", self)
         table_at = _at(page_table, self._i32, "page_table", self)
