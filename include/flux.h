@@ -45,7 +45,7 @@
  *   - A flux_ctx owns the only memory the library allocates (a workspace for
  *     split-KV decode partials and router intermediates, and the error word).
  *     Calls that share a ctx must not overlap in time on different streams
- *     (flux_build_page_table may, beside calls of the others).
+ *     (flux_build_page_table may, beside the other calls).
  *   - flux_last_error() describes the last failure of the calling thread.
  */
 #ifndef FLUX_H
